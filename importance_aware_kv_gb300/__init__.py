@@ -32,7 +32,8 @@ ABI_FUNCTIONS = ("hikv_create_cache", "hikv_destroy_cache", "hikv_append", "hikv
                  "hikv_decode_step_fused", "hikv_kernel_launches", "hikv_budgets_pyramid",
                  "hikv_budgets_duo", "hikv_selftest_timeout", "hikv_element_rows",
                  "hikv_last_decode_config", "hikv_score_band", "hikv_read_floor",
-                 "hikv_read_slot")
+                 "hikv_read_slot", "hikv_append_packed", "hikv_attend_packed", "hikv_drop",
+                 "hikv_device_view")
 
 
 class HikvError(RuntimeError):
@@ -51,6 +52,21 @@ class hikv_config(ctypes.Structure):
                 ("max_window_queries", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("pool_kernel", ctypes.c_int32), ("importance_mode", ctypes.c_int32),
                 ("element_budget", ctypes.c_int32), ("band_scoring", ctypes.c_int32)]
+
+
+class hikv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class hikv_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class hikv_view(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("pool_pages", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32), ("units", ctypes.c_int32),
+                ("importance", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
 
 
 def _load():
@@ -81,6 +97,10 @@ def _load():
         "hikv_selftest_timeout": ([P, I32, P], S),
         "hikv_read_floor": ([P, I64, I32, P, P], S),
         "hikv_read_slot": ([P, I32, I32, P, P, P, P], S),
+        "hikv_append_packed": ([P, I32] + [P] * 7, S),
+        "hikv_attend_packed": ([P, I32] + [P] * 4, S),
+        "hikv_drop": ([P, I32, I32, P, P], S),
+        "hikv_device_view": ([P, ctypes.POINTER(hikv_view)], S),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -151,6 +171,34 @@ def _dev(t, name, dtype=None, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+class Rope:
+    """Rotation tables for Cache.append_packed: cos and sin [positions][r / 2]
+    fp32 on the cache's device, row p for position p; pairs (i, i + r / 2), or
+    (2i, 2i + 1) if interleaved.  Form the angles in 64 bits: an fp32
+    position x frequency is off by up to 2^-24 of the angle, 0.008 rad at
+    position 131072.  Keeps the tables alive."""
+
+    def __init__(self, cos, sin, interleaved: bool = False):
+        import torch
+        _dev(cos, "cos", torch.float32)
+        _dev(sin, "sin", torch.float32, cos.shape)
+        if cos.dim() != 2:
+            raise ValueError(f"cos has shape {tuple(cos.shape)}, expected [positions][rotated / 2]")
+        if cos.device != sin.device:
+            raise ValueError("cos and sin are on different devices")
+        self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self.c = hikv_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+
+
+class _DeviceArray:
+    """Device memory of a cache as a CUDA array; keeps the cache alive."""
+
+    def __init__(self, cache, ptr, shape, typestr):
+        self.cache = cache
+        self.__cuda_array_interface__ = {"data": (ptr, False), "shape": tuple(shape), "typestr": typestr,
+                                         "strides": None, "version": 3}
 
 
 @dataclass
@@ -294,6 +342,8 @@ class Cache:
         self.units_per_layer = cfg.batch * cfg.num_kv_heads
         self.units = cfg.num_layers * self.units_per_layer
         self.h = hikv_create_cache(cfg)
+        import torch
+        self.device_index = torch.cuda.current_device()
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
@@ -331,6 +381,92 @@ class Cache:
         self._check_tensor(k, "k", (nl, c.batch, c.num_kv_heads, ntok, c.head_dim))
         self._check_tensor(v, "v", tuple(k.shape))
         hikv_append(self.h, layer0, k, v, stream)
+
+    def _counts(self, counts, name):
+        """HOST int32 [batch] from a list, array or CPU tensor of whole numbers."""
+        a = np.asarray(counts)
+        if a.dtype.kind not in "iu":
+            raise TypeError(f"{name} must hold whole numbers")
+        if a.shape != (self.cfg.batch,):
+            raise ValueError(f"{name} has shape {a.shape}, expected ({self.cfg.batch},)")
+        if a.size and (a.min() < -1 or a.max() > 0x7FFFFFFF):
+            raise ValueError(f"{name} holds values out of range")
+        return np.ascontiguousarray(a, dtype=np.int32)
+
+    def _rows(self, t, name, total, heads):
+        """Packed rows [tokens][heads][head_dim] as the C ABI's hikv_rows."""
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.device.index != self.device_index:
+            raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device_index}")
+        self._check_tensor(t, name, (total, heads, self.cfg.head_dim))
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        return hikv_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+    def append_packed(self, k, v, ntok, layer=0, q=None, q_out=None, rope=None, stream=None):
+        """Append a packed batch to one layer: k, v [sum ntok][Hkv][d] (any
+        16-byte strides), sequence b's ntok[b] tokens after those of the
+        sequences before it.  With a Rope, k is rotated by position as it
+        enters the cache, and q [sum ntok][Hq][d], if given, into q_out (may
+        be q itself)."""
+        c = self.cfg
+        n = self._counts(ntok, "ntok")
+        total = int(n.sum(dtype=np.int64))
+        rows = [self._rows(k, "k", total, c.num_kv_heads), self._rows(v, "v", total, c.num_kv_heads)]
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        rows += [self._rows(t, name, total, c.num_q_heads) if t is not None else None
+                 for t, name in ((q, "q"), (q_out, "q_out"))]
+        if rope is not None and rope.cos.device.index != self.device_index:
+            raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
+        _check(_lib.hikv_append_packed(self.h, layer, n.ctypes.data, *[ctypes.byref(r) if r else None for r in rows],
+                                       ctypes.byref(rope.c) if rope is not None else None,
+                                       _stream_of(k, stream)))
+
+    def attend_packed(self, q, out, nq, layer=0, stream=None):
+        """Causal attention of the newest nq[b] positions of every sequence
+        over everything its units hold up to them: q, out [sum nq][Hq][d]
+        (any 16-byte strides).  Append the positions' tokens first."""
+        c = self.cfg
+        n = self._counts(nq, "nq")
+        total = int(n.sum(dtype=np.int64))
+        rq, ro = self._rows(q, "q", total, c.num_q_heads), self._rows(out, "out", total, c.num_q_heads)
+        _check(_lib.hikv_attend_packed(self.h, layer, n.ctypes.data, ctypes.byref(rq), ctypes.byref(ro),
+                                       _stream_of(q, stream)))
+
+    def drop(self, counts=None, layer0=0, nlayers=None, stream=None):
+        """Drop the newest counts[b] tokens of every unit of batch row b (-1,
+        or counts None: all); their positions are free again."""
+        n = None if counts is None else self._counts(counts, "counts")
+        nl = self.cfg.num_layers - layer0 if nlayers is None else nlayers
+        _check(_lib.hikv_drop(self.h, layer0, nl, None if n is None else n.ctypes.data, self._own_stream(stream)))
+
+    def _own_stream(self, stream):
+        import torch
+        return _stream(torch.cuda.current_stream(self.device_index) if stream is None else stream)
+
+    def device_view(self) -> dict:
+        """The cache's own device memory as tensors, without a copy: pages
+        [pool_pages][2 (K, V)][page_tokens][d], page_table [units][max_pages],
+        importance and positions [units][max_tokens] by slot, lengths
+        [units].  Valid until close(); order reads after the calls that write."""
+        import torch
+        c, w = self.cfg, hikv_view()
+        _check(_lib.hikv_device_view(self.h, ctypes.byref(w)))
+        pt = c.page_tokens or 64
+        bf16 = c.dtype == "bf16"
+
+        def arr(ptr, shape, typestr):
+            return torch.as_tensor(_DeviceArray(self, ptr, shape, typestr), device=f"cuda:{self.device_index}")
+
+        pages = arr(w.pool, (w.pool_pages, 2, pt, c.head_dim), "<i2" if bf16 else "<f4")
+        return {"pages": pages.view(torch.bfloat16) if bf16 else pages,
+                "page_table": arr(w.page_table, (w.units, w.max_pages), "<i4"),
+                "importance": arr(w.importance, (w.units, c.max_tokens), "<f4"),
+                "positions": arr(w.positions, (w.units, c.max_tokens), "<i4"),
+                "lengths": arr(w.lengths, (w.units,), "<i4")}
 
     def score_window(self, q, layer0=0, stream=None):
         c = self.cfg

@@ -172,6 +172,36 @@ __device__ __forceinline__ uint8_t* row_ptr(const View& v, int32_t u, int32_t s,
            ((is_v ? (int64_t)v.page_tokens : 0) + r) * v.row_bytes;
 }
 
+// Per unit: reserve ntok slots and map the pages they need.  Writes the
+// first slot to base[u - u0] (-1 when the pool ran dry, which the host's
+// capacity check makes impossible).
+__device__ inline void reserve_unit(const View& v, int32_t u, int32_t ntok, int32_t* base_out) {
+    int32_t n = v.len[u];
+    int32_t need = ceil_div(n + ntok, v.page_tokens);
+    int32_t m = v.mapped[u];
+    if (n + ntok > v.cap || need > v.max_pages) {
+        atomicOr(v.err, DEVERR_STATE);
+        *base_out = -1;
+        return;
+    }
+    if (need > m) {
+        int32_t cnt = need - m;
+        int32_t old = atomicSub(v.free_top, cnt);
+        if (old - cnt < 0) {
+            atomicAdd(v.free_top, cnt);
+            atomicOr(v.err, DEVERR_POOL);
+            *base_out = -1;
+            return;
+        }
+        for (int32_t i = 0; i < cnt; ++i)
+            v.page_table[(int64_t)u * v.max_pages + m + i] = v.free_stack[old - cnt + i];
+        v.mapped[u] = need;
+    }
+    *base_out = n;
+    v.len[u] = n + ntok;
+    v.next_pos[u] += ntok;
+}
+
 // ---------------------------------------------------------------------------
 // PTX wrappers (sm_90+ mbarrier / bulk copy / cluster; used on sm_103a)
 // ---------------------------------------------------------------------------
@@ -538,6 +568,56 @@ struct AppendArgs {
     int32_t* base;   // scratch [units]: first slot of this append per unit
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+
+// A packed batch of one layer in kernel parameters: up to kSeqMax sequences,
+// batch rows row0 .. row0 + n, sequence i's tokens at packed rows
+// [start[i], start[i + 1]).  Parameters are copied with the launch, so calls
+// need no device copy of the lengths and may be captured into a graph; longer
+// batches take one launch per kSeqMax sequences.
+constexpr int kSeqMax = 256;
+struct PackedSeqs {
+    int32_t n, row0;
+    int32_t start[kSeqMax + 1];
+};
+// rows (t, h) of packed tensors, strides in bytes
+struct RowsArg {
+    uint8_t* p;
+    int64_t ts, hs;
+    __device__ __forceinline__ uint8_t* row(int64_t t, int32_t h) const { return p + t * ts + (int64_t)h * hs; }
+};
+struct PackedAppendArgs {
+    View v;
+    PackedSeqs seqs;
+    int32_t u0;             // unit of (the layer, batch row 0, KV head 0)
+    RowsArg k, vv, q, qo;   // q.p null: no queries
+    const float* cos;       // null: no rotation
+    const float* sin;
+    int32_t rot, interleaved;
+    int32_t* base;          // scratch [units]: first slot of this append
+};
+cudaError_t launch_append_packed(const PackedAppendArgs& a, int dtype, cudaStream_t s);
+
+// Causal attention of packed queries over the cache (hikv_attend_packed)
+struct AttendArgs {
+    View v;
+    PackedSeqs seqs;
+    int32_t u0;             // unit of (the layer, batch row 0, KV head 0)
+    int32_t gshift;         // log2 of the query heads per KV head
+    RowsArg q, out;
+    float qscale;           // scale * log2(e)
+    int32_t items;          // work items of the launch: tiles of query rows x KV heads
+    int32_t tile0[kSeqMax + 1];   // first row tile of each sequence (row = token * G + head of the group)
+};
+cudaError_t launch_attend_simt(const AttendArgs& a, int dtype, int d, cudaStream_t s);
+constexpr int kSimtRows = 64;   // query rows of a tile of that kernel
+
+constexpr int kDropMax = 512;
+struct DropArgs {
+    View v;
+    int32_t layer0, nlayers, row0, n;   // batch rows row0 .. row0 + n of every layer of the range
+    int32_t count[kDropMax];            // tokens to drop, -1: all
+};
+cudaError_t launch_drop(const DropArgs& a, cudaStream_t s);
 
 struct DecodeArgs {
     View v;

@@ -1,0 +1,269 @@
+// Host side of the packed-batch entry points: a layer's tokens of sequences
+// of different lengths appended, attended with and dropped again.  Checks,
+// the host mirror and the launches, as in hikv_host.cu.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "hikv_cache.cuh"
+
+using namespace hikv;
+
+namespace {
+
+// What is wrong with packed rows, or null.  `distinct`: written rows, which
+// must not overlap one another.
+const char* rows_fault(const hikv_cache* c, const hikv_rows* r, int64_t total, int heads, bool distinct) {
+    const int64_t e = c->esz;
+    if (!r->data) return "null data";
+    if ((uintptr_t)r->data & 15) return "data not 16-byte aligned";
+    if (r->token_stride < 0 || r->head_stride < 0) return "a negative stride";
+    if (r->token_stride > (INT64_MAX >> 32) || r->head_stride > (INT64_MAX >> 32)) return "a stride too large";
+    if (r->token_stride * e % 16 || r->head_stride * e % 16) return "a stride that is no multiple of 16 bytes";
+    if (distinct) {
+        const int64_t d = c->d, ts = r->token_stride, hs = r->head_stride;
+        const bool heads_inside = (heads == 1 || hs >= d) && (total <= 1 || ts >= (heads - 1) * hs + d);
+        const bool tokens_inside = (total <= 1 || ts >= d) && (heads == 1 || hs >= (total - 1) * ts + d);
+        if (!heads_inside && !tokens_inside) return "rows that overlap one another";
+    }
+    return nullptr;
+}
+
+RowsArg rows_arg(const hikv_cache* c, const hikv_rows* r) {
+    return {(uint8_t*)r->data, r->token_stride * c->esz, r->head_stride * c->esz};
+}
+
+// Packed token counts of a call: their sum, or -1 when one is negative or
+// the sum passes 32 bits.
+int64_t packed_total(const hikv_cache* c, const int32_t* ntok) {
+    int64_t total = 0;
+    for (int b = 0; b < c->B; ++b) {
+        if (ntok[b] < 0) return -1;
+        total += ntok[b];
+    }
+    return total <= INT32_MAX ? total : -1;
+}
+
+}  // namespace
+
+extern "C" {
+
+hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok, const hikv_rows* k,
+                               const hikv_rows* vv, const hikv_rows* q, const hikv_rows* q_out,
+                               const hikv_rope* rope, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_append_packed");
+    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "append_packed: bad cache or layer");
+    if (!ntok || !k || !vv) return fail(HIKV_ERR_INVALID_ARG, "append_packed: null ntok, k or v");
+    const int64_t total = packed_total(c, ntok);
+    if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "append_packed: a token count is negative or their sum too large");
+    if (total == 0) return HIKV_OK;
+    if ((q != nullptr) != (q_out != nullptr))
+        return fail(HIKV_ERR_INVALID_ARG, "append_packed: q and q_out go together");
+    if (q && !rope) return fail(HIKV_ERR_INVALID_ARG, "append_packed: q without a rope");
+    const char* bad = nullptr;
+    if ((bad = rows_fault(c, k, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: k has %s", bad);
+    if ((bad = rows_fault(c, vv, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: v has %s", bad);
+    if (q) {
+        if ((bad = rows_fault(c, q, total, c->Hq, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: q has %s", bad);
+        if ((bad = rows_fault(c, q_out, total, c->Hq, true)))
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out has %s", bad);
+        if (q->data == q_out->data && (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out in the place of q needs its strides");
+    }
+    if (rope) {
+        if (!rope->cos || !rope->sin || (((uintptr_t)rope->cos | (uintptr_t)rope->sin) & 15))
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: null or misaligned rope tables");
+        if (rope->interleaved != 0 && rope->interleaved != 1)
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: interleaved %d not in {0, 1}", rope->interleaved);
+        if (rope->rot_dim < 16 || rope->rot_dim > c->d || rope->rot_dim % 16)
+            return fail(HIKV_ERR_UNSUPPORTED, "append_packed: rot_dim %d is no multiple of 16 up to head_dim %d",
+                        rope->rot_dim, c->d);
+    }
+    const int u0 = layer * c->per_layer;
+    int64_t new_pages = 0;
+    for (int b = 0; b < c->B; ++b) {
+        if (ntok[b] == 0) continue;
+        const int ub = u0 + b * c->Hkv;
+        for (int u = ub; u < ub + c->Hkv; ++u) {
+            if ((int64_t)c->len[u] + ntok[b] > c->cap)
+                return fail(HIKV_ERR_CAPACITY, "append_packed: unit %d would hold %lld > max_tokens %d", u,
+                            (long long)c->len[u] + ntok[b], c->cap);
+            if (c->next_pos[u] != c->next_pos[ub])
+                return fail(HIKV_ERR_STATE, "append_packed: units %d and %d are at different positions", u, ub);
+            new_pages += std::max(0, ceil_div(c->len[u] + ntok[b], c->P) - c->mapped[u]);
+        }
+        const int64_t end = (int64_t)c->next_pos[ub] + ntok[b];
+        if (end > INT32_MAX) return fail(HIKV_ERR_CAPACITY, "append_packed: positions of batch row %d overflow int32", b);
+        if (rope && end > rope->positions)
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: batch row %d reaches position %lld, the rope has %d", b,
+                        (long long)end - 1, rope->positions);
+    }
+    if (c->pages_in_use + new_pages > c->pool_pages)
+        return fail(HIKV_ERR_CAPACITY, "append_packed: page pool exhausted (%lld in use + %lld > %lld)",
+                    (long long)c->pages_in_use, (long long)new_pages, (long long)c->pool_pages);
+    DeviceGuard guard(c->device);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "append_packed: device");
+    pdl_forget(c);
+    PackedAppendArgs a{};
+    a.v = c->v;
+    a.u0 = u0;
+    a.k = rows_arg(c, k);
+    a.vv = rows_arg(c, vv);
+    if (q) {
+        a.q = rows_arg(c, q);
+        a.qo = rows_arg(c, q_out);
+    }
+    if (rope) {
+        a.cos = rope->cos;
+        a.sin = rope->sin;
+        a.rot = rope->rot_dim;
+        a.interleaved = rope->interleaved;
+    }
+    a.base = c->d_append_base;
+    int32_t row = 0;
+    for (int b0 = 0; b0 < c->B; b0 += kSeqMax) {
+        const int n = std::min(kSeqMax, c->B - b0);
+        a.seqs.n = n;
+        a.seqs.row0 = b0;
+        for (int i = 0; i < n; ++i) {
+            a.seqs.start[i] = row;
+            row += ntok[b0 + i];
+        }
+        a.seqs.start[n] = row;
+        if (row == a.seqs.start[0]) continue;
+        cudaError_t e = launch_append_packed(a, c->dtype, (cudaStream_t)stream);
+        c->launches += 2;
+        if (e != cudaSuccess) return cuda_fail(e, "append_packed: launch");
+        for (int i = 0; i < n * c->Hkv; ++i) {
+            const int u = u0 + b0 * c->Hkv + i, m = ntok[b0 + i / c->Hkv];
+            if (m == 0) continue;
+            c->len[u] += m;
+            c->next_pos[u] += m;
+            c->tail[u] += m;
+            const int mapped = std::max(c->mapped[u], ceil_div(c->len[u], c->P));
+            c->pages_in_use += mapped - c->mapped[u];
+            c->mapped[u] = mapped;
+            c->fresh[u] = 0;
+        }
+    }
+    return HIKV_OK;
+}
+
+hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, const hikv_rows* q,
+                               const hikv_rows* out, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_attend_packed");
+    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: bad cache or layer");
+    if (!nq || !q || !out) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: null nq, q or out");
+    const int64_t total = packed_total(c, nq);
+    if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: a query count is negative or their sum too large");
+    if (total == 0) return HIKV_OK;
+    const char* bad = nullptr;
+    if ((bad = rows_fault(c, q, total, c->Hq, false))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
+    if ((bad = rows_fault(c, out, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out has %s", bad);
+    if (q->data == out->data) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out aliases q");
+    const int u0 = layer * c->per_layer;
+    for (int i = 0; i < c->per_layer; ++i)
+        if (nq[i / c->Hkv] > c->tail[u0 + i])
+            return fail(HIKV_ERR_STATE, "attend_packed: %d queries of unit %d, which holds its newest %d in order",
+                        nq[i / c->Hkv], u0 + i, c->tail[u0 + i]);
+    DeviceGuard guard(c->device);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
+    pdl_forget(c);
+    AttendArgs a{};
+    a.v = c->v;
+    a.u0 = u0;
+    while ((1 << a.gshift) < c->G) ++a.gshift;
+    a.q = rows_arg(c, q);
+    a.out = rows_arg(c, out);
+    a.qscale = c->scale * 1.4426950408889634f;
+    int32_t row = 0;
+    for (int b0 = 0; b0 < c->B; b0 += kSeqMax) {
+        const int n = std::min(kSeqMax, c->B - b0);
+        a.seqs.n = n;
+        a.seqs.row0 = b0;
+        int64_t tiles = 0;
+        for (int i = 0; i < n; ++i) {
+            a.seqs.start[i] = row;
+            a.tile0[i] = (int32_t)tiles;
+            row += nq[b0 + i];
+            tiles += ((int64_t)nq[b0 + i] * c->G + kSimtRows - 1) / kSimtRows;
+        }
+        a.seqs.start[n] = row;
+        a.tile0[n] = (int32_t)tiles;
+        if (tiles == 0) continue;
+        if (tiles * c->Hkv > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
+        a.items = (int32_t)(tiles * c->Hkv);
+        cudaError_t e = launch_attend_simt(a, c->dtype, c->d, (cudaStream_t)stream);
+        c->launches += 1;
+        if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");
+    }
+    return HIKV_OK;
+}
+
+hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* ndrop, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_drop");
+    if (!range_ok(c, layer0, nl)) return fail(HIKV_ERR_INVALID_ARG, "drop: bad cache or layer range");
+    const int u0 = layer0 * c->per_layer, nu = nl * c->per_layer;
+    auto count = [&](int b) { return ndrop ? ndrop[b] : -1; };
+    bool any = false;
+    for (int b = 0; b < c->B; ++b) {
+        if (count(b) < -1) return fail(HIKV_ERR_INVALID_ARG, "drop: %d tokens of batch row %d", count(b), b);
+        any |= count(b) != 0;
+    }
+    if (!any) return HIKV_OK;
+    for (int u = u0; u < u0 + nu; ++u) {
+        const int n = count(u % c->per_layer / c->Hkv);
+        if (n > c->tail[u])
+            return fail(HIKV_ERR_STATE, "drop: %d tokens of unit %d, which holds its newest %d in order", n, u, c->tail[u]);
+    }
+    DeviceGuard guard(c->device);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "drop: device");
+    pdl_forget(c);
+    DropArgs a{};
+    a.v = c->v;
+    a.layer0 = layer0;
+    a.nlayers = nl;
+    for (int b0 = 0; b0 < c->B; b0 += kDropMax) {
+        a.row0 = b0;
+        a.n = std::min(kDropMax, c->B - b0);
+        for (int i = 0; i < a.n; ++i) a.count[i] = count(b0 + i);
+        cudaError_t e = launch_drop(a, (cudaStream_t)stream);
+        c->launches += 1;
+        if (e != cudaSuccess) return cuda_fail(e, "drop: launch");
+    }
+    for (int u = u0; u < u0 + nu; ++u) {
+        const int n = count(u % c->per_layer / c->Hkv);
+        if (n == 0) continue;
+        c->len[u] = n < 0 ? 0 : c->len[u] - n;
+        c->next_pos[u] = n < 0 ? 0 : c->next_pos[u] - n;
+        c->tail[u] = n < 0 ? 0 : c->tail[u] - n;
+        c->fresh[u] = 0;
+        if (!c->v.home_pages) {
+            const int mapped = std::min(c->mapped[u], ceil_div(c->len[u], c->P));
+            c->pages_in_use -= c->mapped[u] - mapped;
+            c->mapped[u] = mapped;
+        }
+    }
+    return HIKV_OK;
+}
+
+hikv_status hikv_device_view(const hikv_cache* c, hikv_view* out) {
+    set_last_error("");
+    if (!c || !out) return fail(HIKV_ERR_INVALID_ARG, "device_view: null cache or output");
+    *out = hikv_view{};
+    out->pool = c->v.pool;
+    out->page_bytes = c->v.page_bytes;
+    out->pool_pages = c->pool_pages;
+    out->page_table = c->v.page_table;
+    out->max_pages = c->max_pages;
+    out->units = c->units;
+    out->importance = c->v.imp;
+    out->positions = c->v.pos;
+    out->lengths = c->v.len;
+    return HIKV_OK;
+}
+
+}  // extern "C"

@@ -11,36 +11,6 @@
 namespace hikv {
 namespace {
 
-// Per unit: reserve ntok slots and map the pages they need.  Writes the
-// first slot to base[u - u0] (-1 when the pool ran dry, which the host's
-// capacity check makes impossible).
-__device__ void reserve_unit(const View& v, int32_t u, int32_t ntok, int32_t* base_out) {
-    int32_t n = v.len[u];
-    int32_t need = ceil_div(n + ntok, v.page_tokens);
-    int32_t m = v.mapped[u];
-    if (n + ntok > v.cap || need > v.max_pages) {
-        atomicOr(v.err, DEVERR_STATE);
-        *base_out = -1;
-        return;
-    }
-    if (need > m) {
-        int32_t cnt = need - m;
-        int32_t old = atomicSub(v.free_top, cnt);
-        if (old - cnt < 0) {
-            atomicAdd(v.free_top, cnt);
-            atomicOr(v.err, DEVERR_POOL);
-            *base_out = -1;
-            return;
-        }
-        for (int32_t i = 0; i < cnt; ++i)
-            v.page_table[(int64_t)u * v.max_pages + m + i] = v.free_stack[old - cnt + i];
-        v.mapped[u] = need;
-    }
-    *base_out = n;
-    v.len[u] = n + ntok;
-    v.next_pos[u] += ntok;
-}
-
 __device__ void copy_rows(const View& v, int32_t u, int32_t slot0, int32_t pos0,
                           const uint8_t* ksrc, const uint8_t* vsrc, int32_t r0, int32_t r1) {
     const int32_t vec_per_row = v.row_bytes / 16;

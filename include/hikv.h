@@ -294,6 +294,108 @@ int64_t hikv_kernel_launches(const hikv_cache* cache);
  * error, else OK. */
 hikv_status hikv_device_status(hikv_cache* cache);
 
+/* Rows of packed tensors: row (t, h) -- token t of the packed batch, head h --
+ * is head_dim contiguous elements of the cache dtype at
+ * data + (t * token_stride + h * head_stride) elements.  data (DEVICE) must be
+ * 16-byte aligned and both strides a multiple of 16 bytes, so that the q, k
+ * and v slices of one projection's output can be passed as they are. */
+typedef struct {
+    void* data;
+    int64_t token_stride;   /* elements */
+    int64_t head_stride;    /* elements */
+} hikv_rows;
+
+/* Rotary position embedding: cos and sin (DEVICE fp32, contiguous, 16-byte
+ * aligned) [positions][rot_dim / 2]; row p is position p's.  The first rot_dim
+ * elements of a row are rotated in pairs, the rest pass unchanged: pair i is
+ * elements (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved = 1, and
+ *     a' = a cos[p][i] - b sin[p][i],   b' = b cos[p][i] + a sin[p][i],
+ * formed in fp32 and rounded once to the cache dtype. */
+typedef struct {
+    const float* cos;
+    const float* sin;
+    int32_t positions;
+    int32_t rot_dim;        /* multiple of 16, <= head_dim */
+    int32_t interleaved;    /* 0 or 1 */
+} hikv_rope;
+
+/* Append a packed batch to one layer, each sequence its own number of tokens,
+ * with the position rotation on the way: sequence (batch row) b adds
+ * ntok_host[b] >= 0 tokens (HOST, [batch]; read before the call returns) to
+ * its units of layer `layer`; the tokens of all sequences lie one sequence
+ * after the other in the rows of k and v ([sum ntok][Hkv] rows).  With a
+ * rope, k is rotated by the position each token gets (its unit's next one)
+ * as it enters the cache, v enters as it is, and, if q is given
+ * ([sum ntok][Hq] rows), the rotated q goes to q_out, which may be q itself
+ * and must not overlap anything else.  rope NULL: k enters as it is; q must
+ * then be NULL.  New tokens get importance 0, as by hikv_append.
+ * A sequence's KV heads may hold different numbers of tokens (budgets by
+ * head), but must have seen the same number of positions.
+ * Capture: the call may be captured into a CUDA graph.  The host mirror
+ * advances once, at the capture; replay the graph only where every unit of the layer
+ * holds what it held at the capture (with a hikv_drop captured in front, say).
+ * Errors: INVALID_ARG (null or misaligned pointers, strides, ntok < 0, a rope
+ * whose table ends before the last position, q_out rows that overlap one
+ * another), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append). */
+hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* ntok_host,
+                               const hikv_rows* k, const hikv_rows* v, const hikv_rows* q,
+                               const hikv_rows* q_out, const hikv_rope* rope, hikv_stream_t stream);
+
+/* Causal attention of a packed batch of queries over the cache: the queries of
+ * the newest nq_host[b] >= 0 positions of sequence b (HOST, [batch]; read
+ * before the call returns), one sequence after the other in the rows of q
+ * ([sum nq][Hq] rows), each over everything its unit holds up to its own
+ * position:
+ *     out_i = sum_{s <= n - nq + i} softmax_s(scale q_i . k_s) v_s,
+ * slot s of a unit of n tokens, query head h reading KV head h / G.  For
+ * whole prompts (nq = n), the next chunk of a prompt over what is cached
+ * (which may have been cut, to another length for every head), the tokens of
+ * a speculative verification, or one token; append them first.  Neither
+ * importance nor any other state changes (hikv_score_window and
+ * hikv_decode_step score).  Softmax statistics and sums are fp32.  A K or V
+ * row that a query does not see does not touch its output, whatever it holds.
+ * out: [sum nq][Hq] rows, written; must not overlap q.  Always exact
+ * attention, with an element_budget too.  May be captured as
+ * hikv_append_packed.
+ * Errors: INVALID_ARG (null or misaligned pointers, strides, nq < 0), STATE
+ * (more queries than the unit holds newest positions in order: the tokens it
+ * holds, or those appended since its last cut). */
+hikv_status hikv_attend_packed(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const hikv_rows* q,
+                               const hikv_rows* out, hikv_stream_t stream);
+
+/* Drop the newest tokens: ndrop_host[b] of every unit of batch row b in the
+ * layer range (HOST, [batch]; -1: all the unit holds; ndrop_host NULL: -1 for
+ * every row).  The dropped positions are free again: the next appended token
+ * takes the first of them, position 0 after a drop of all.  For tokens a
+ * verification rejected, and to take the next batch of prompts without a
+ * new cache.  Importance that the dropped tokens' queries added to others
+ * stays.  A unit that was cut can drop the tokens appended since its last cut
+ * (a cut reorders the others), or all.  With a shared pool whole pages past the
+ * remaining tokens return to it.  May be captured as hikv_append_packed.
+ * Errors: INVALID_ARG (ndrop < -1), STATE (more than the unit holds in order). */
+hikv_status hikv_drop(hikv_cache* cache, int32_t layer0, int32_t nlayers, const int32_t* ndrop_host,
+                      hikv_stream_t stream);
+
+/* The cache's own device memory, for callers that move or inspect pages
+ * without a copy (device pointers, valid until hikv_destroy_cache; reads must
+ * be ordered after the calls that write).  Page p is page_bytes at
+ * pool + p * page_bytes: K rows [page_tokens][head_dim], then V rows.  Slot s
+ * of unit u is row s % page_tokens of page page_table[u][s / page_tokens] (-1:
+ * none); importance and positions are [units][max_tokens] by slot, lengths
+ * [units].  Host only.  Errors: INVALID_ARG. */
+typedef struct {
+    void* pool;
+    int64_t page_bytes;
+    int64_t pool_pages;
+    int32_t* page_table;    /* [units][max_pages] */
+    int32_t max_pages;
+    int32_t units;
+    float* importance;
+    int32_t* positions;
+    int32_t* lengths;
+} hikv_view;
+hikv_status hikv_device_view(const hikv_cache* cache, hikv_view* out);
+
 /* Prompt importance for callers that cannot allocate device memory.
  *
  * The pages have no counterpart of this entry point; it exists for callers
