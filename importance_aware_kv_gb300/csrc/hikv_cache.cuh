@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -54,6 +55,7 @@ struct hikv_cache {
     int first_burst = 4;                // one tile per consumer warp first (HIKV_DECODE_BURST: tuning)
     int prefetch_override = -1;         // HIKV_DECODE_PREFETCH (tuning): L2 prefetch distance in tiles, -1 auto
     CUtensorMap tmap;                   // the pool as rows of d elements, 16 x 128-byte swizzled boxes
+    CUtensorMap tmap_page;              // the same with boxes of min(P, 128) rows (bf16: packed attention)
     std::vector<void*> allocs;
     // host mirror
     std::vector<int32_t> len, next_pos, mapped;
@@ -103,6 +105,9 @@ struct NvtxRange {
 hikv_status fail(hikv_status s, const char* fmt, ...);
 hikv_status cuda_fail(cudaError_t e, const char* what);
 void set_last_error(const char* msg);
+
+// cuTensorMapEncodeTiled from the driver, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 inline void pdl_forget(hikv_cache* c) { if (c) c->pdl_valid = false; }
 

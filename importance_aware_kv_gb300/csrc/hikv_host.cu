@@ -52,12 +52,6 @@ hikv_status cuda_fail(cudaError_t e, const char* what) {
     return fail(HIKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-}  // namespace hikv
-
-namespace {
-
-constexpr int kWindowChunk = 1024;   // tokens per CTA of the window-scoring kernels
-
 // cuTensorMapEncodeTiled from the driver, found through the runtime (no
 // link-time dependency on libcuda).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -72,6 +66,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     }
     return fn;
 }
+
+}  // namespace hikv
+
+namespace {
+
+constexpr int kWindowChunk = 1024;   // tokens per CTA of the window-scoring kernels
 
 }  // namespace
 
@@ -303,6 +303,12 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
                          2, v.pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r == CUDA_SUCCESS && c->dtype == HIKV_BF16) {
+            box[1] = (cuuint32_t)std::min(P, 128);
+            r = enc(&c->tmap_page, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v.pool, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        }
         if (r != CUDA_SUCCESS) {
             free_all(c);
             delete c;
@@ -1105,10 +1111,10 @@ hikv_status hikv_device_status(hikv_cache* c) {
     if (w[0] & DEVERR_TIMEOUT) {
         static const char* const sites[] = {"?", "producer q-free", "producer stage-free", "producer drain",
                                             "consumer q", "consumer tile", "cluster exchange", "victim exchange",
-                                            "self-test"};
+                                            "self-test", "packed attention"};
         return fail(HIKV_ERR_TIMEOUT,
                     "device: a bounded wait gave up (bits 0x%x; first: %s wait, cluster %u, CTA %u, index 0x%x, "
-                    "after %u us)", w[0], sites[w[1] < 9 ? w[1] : 0], w[2], w[3], w[4], w[5]);
+                    "after %u us)", w[0], sites[w[1] < 10 ? w[1] : 0], w[2], w[3], w[4], w[5]);
     }
     if (w[0]) return fail(HIKV_ERR_STATE, "device: inconsistent state recorded (bits 0x%x)", w[0]);
     return HIKV_OK;

@@ -296,7 +296,7 @@ __device__ __forceinline__ uint64_t global_ns() {
 // site-specific index, err[5] = microseconds waited.
 enum : uint32_t {
     kWaitQEmpty = 1, kWaitEmpty = 2, kWaitDrain = 3, kWaitQFull = 4, kWaitFull = 5, kWaitXchg = 6,
-    kWaitVictim = 7, kWaitSelftest = 8
+    kWaitVictim = 7, kWaitSelftest = 8, kWaitAttend = 9
 };
 __device__ __forceinline__ void record_timeout(uint32_t* err, uint32_t site, uint32_t extra, uint64_t waited_ns) {
     atomicOr(err, DEVERR_TIMEOUT);
@@ -352,6 +352,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tmap, 
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
             smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 3-D tiled TMA load of box {x, y, z} of `tmap` into shared memory.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tmap, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -597,19 +607,48 @@ struct PackedAppendArgs {
 };
 cudaError_t launch_append_packed(const PackedAppendArgs& a, int dtype, cudaStream_t s);
 
-// Causal attention of packed queries over the cache (hikv_attend_packed)
+// Causal attention of packed queries over the cache (hikv_attend_packed).
+// Query row r of a (sequence, KV head) is token r / G, head r % G of its
+// group: the G heads that read one KV head share its tiles.  A work item is
+// (sequence, tile of query rows, split of the keys, KV head), numbered
+// sequence by sequence (longest first) and in a sequence from its last tile,
+// which sees most, to its first.  As the packed batch above, the sequences
+// come in kernel parameters.
+constexpr int kAttSeqs = 160;
 struct AttendArgs {
     View v;
-    PackedSeqs seqs;
     int32_t u0;             // unit of (the layer, batch row 0, KV head 0)
-    int32_t gshift;         // log2 of the query heads per KV head
+    int32_t gshift;         // log2(G)
     RowsArg q, out;
     float qscale;           // scale * log2(e)
-    int32_t items;          // work items of the launch: tiles of query rows x KV heads
-    int32_t tile0[kSeqMax + 1];   // first row tile of each sequence (row = token * G + head of the group)
+    int32_t chunk;          // keys per split (a multiple of 128)
+    float* part;            // partial results of split items: [splits][part_rows][d] outputs, ...
+    float* part_ml;         // ... [splits][part_rows][2] maxima and sums
+    int64_t part_rows;      // rows (t, h) of the packed batch
+    int32_t nseq, items;
+    int32_t brow[kAttSeqs];        // batch row
+    int32_t start[kAttSeqs];       // first packed row
+    int32_t nq[kAttSeqs];          // queries
+    int32_t item0[kAttSeqs + 1];   // first work item
+    int32_t comb0[kAttSeqs + 1];   // tokens of the sequences before it whose items are split
 };
-cudaError_t launch_attend_simt(const AttendArgs& a, int dtype, int d, cudaStream_t s);
-constexpr int kSimtRows = 64;   // query rows of a tile of that kernel
+// the sequence that holds element x of a prefix table
+__device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (first[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s);
+constexpr int kSimtRows = 64;   // query rows of a work item of that kernel
+cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
+                             int n_ctas, cudaStream_t s);
+constexpr int kTcRows = 256;    // of the tensor-core kernel
+constexpr int kTcKeys = 128;    // keys per tile
+cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s);
 
 constexpr int kDropMax = 512;
 struct DropArgs {

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <vector>
 
 #include "hikv_cache.cuh"
 
@@ -42,6 +43,51 @@ int64_t packed_total(const hikv_cache* c, const int32_t* ntok) {
         total += ntok[b];
     }
     return total <= INT32_MAX ? total : -1;
+}
+
+// Keys per split of a tensor-core launch, a multiple of the key tile
+// (INT32_MAX: no split).  A CTA works through its items at about one key tile
+// a step and spends about kItemSteps more on each (its first loads, its
+// epilogue); the splits' partial results cost a second launch and their
+// traffic.  The candidates cut the longest sequence into 1 .. 64 parts.
+template <class Seq>
+int32_t attend_chunk(const hikv_cache* c, const Seq* sq, int nseq, int64_t total) {
+    constexpr double kItemSteps = 3.0, kJoinSteps = 4.0;
+    const int64_t maxsteps = ceil_div(sq[0].n, kTcKeys);
+    int64_t base_items = 0;
+    for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + kTcRows - 1) / kTcRows) * c->Hkv;
+    if (base_items >= 4 * (int64_t)c->sm_count) return INT32_MAX;
+    const int64_t room = (int64_t)c->units * c->cap * c->G;   // floats of the work buffer
+    double best = 0;
+    int32_t best_chunk = INT32_MAX;
+    int64_t last = 0;
+    for (int k = 1; k <= 64; ++k) {
+        const int64_t ct = (maxsteps + k - 1) / k;   // key tiles per split
+        if (ct == last || (k > 1 && ct < 2)) continue;
+        last = ct;
+        const int64_t splits = (maxsteps + ct - 1) / ct;
+        if (splits > 1 && splits * total * c->Hq * (c->d + 2) > room) break;
+        int64_t items = 0;
+        double steps = 0, longest = 0;
+        for (int i = 0; i < nseq; ++i) {
+            const int64_t tiles = ((int64_t)sq[i].nq * c->G + kTcRows - 1) / kTcRows;
+            for (int64_t t = 0; t < tiles; ++t) {
+                const int64_t seen = sq[i].n - sq[i].nq + std::min<int64_t>(sq[i].nq, (t + 1) * kTcRows / c->G);
+                const int64_t st = (seen + kTcKeys - 1) / kTcKeys;
+                items += (st + ct - 1) / ct * c->Hkv;
+                steps += (double)st * c->Hkv;
+                longest = std::max(longest, (double)std::min(st, ct));
+            }
+        }
+        double cost = std::max((steps + items * kItemSteps) / c->sm_count, longest + kItemSteps);
+        if (items > c->sm_count) cost += 0.5 * longest;
+        if (splits > 1) cost += kJoinSteps;
+        if (k == 1 || cost < best) {
+            best = cost;
+            best_chunk = splits > 1 ? (int32_t)(ct * kTcKeys) : INT32_MAX;
+        }
+    }
+    return best_chunk;
 }
 
 }  // namespace
@@ -160,7 +206,7 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
     if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: a query count is negative or their sum too large");
     if (total == 0) return HIKV_OK;
     const char* bad = nullptr;
-    if ((bad = rows_fault(c, q, total, c->Hq, false))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
+    if ((bad = rows_fault(c, q, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
     if ((bad = rows_fault(c, out, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out has %s", bad);
     if (q->data == out->data) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out aliases q");
     const int u0 = layer * c->per_layer;
@@ -171,6 +217,22 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
     DeviceGuard guard(c->device);
     if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
     pdl_forget(c);
+    if (total * c->Hq > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
+    const bool tc = c->dtype == HIKV_BF16;
+    CUtensorMap qmap;
+    if (tc) {
+        // q as [tokens][heads][d], boxes of 128 query rows x 128 bytes
+        cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->Hq, (cuuint64_t)total};
+        cuuint64_t strides[2] = {(cuuint64_t)(c->Hq > 1 ? q->head_stride : c->d) * 2,
+                                 (cuuint64_t)(total > 1 ? q->token_stride : c->d) * 2};
+        cuuint32_t box[3] = {64u, (cuuint32_t)c->G, (cuuint32_t)(128 / c->G)};
+        cuuint32_t estr[3] = {1u, 1u, 1u};
+        const CUresult r = tensor_map_encoder()(
+            &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: no tensor map of q (%d)", (int)r);
+    }
     AttendArgs a{};
     a.v = c->v;
     a.u0 = u0;
@@ -178,25 +240,47 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
     a.q = rows_arg(c, q);
     a.out = rows_arg(c, out);
     a.qscale = c->scale * 1.4426950408889634f;
-    int32_t row = 0;
-    for (int b0 = 0; b0 < c->B; b0 += kSeqMax) {
-        const int n = std::min(kSeqMax, c->B - b0);
-        a.seqs.n = n;
-        a.seqs.row0 = b0;
-        int64_t tiles = 0;
-        for (int i = 0; i < n; ++i) {
-            a.seqs.start[i] = row;
-            a.tile0[i] = (int32_t)tiles;
-            row += nq[b0 + i];
-            tiles += ((int64_t)nq[b0 + i] * c->G + kSimtRows - 1) / kSimtRows;
+    a.part_rows = total * c->Hq;
+    // the sequences with queries, longest first: the work items start with the heaviest
+    struct Seq { int32_t brow, start, nq, n; };
+    std::vector<Seq> seqs;
+    for (int b = 0, row = 0; b < c->B; row += nq[b++])
+        if (nq[b] > 0) {
+            const int32_t* len = c->len.data() + u0 + b * c->Hkv;
+            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
         }
-        a.seqs.start[n] = row;
-        a.tile0[n] = (int32_t)tiles;
-        if (tiles == 0) continue;
-        if (tiles * c->Hkv > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
-        a.items = (int32_t)(tiles * c->Hkv);
-        cudaError_t e = launch_attend_simt(a, c->dtype, c->d, (cudaStream_t)stream);
+    std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
+    const int rows = tc ? kTcRows : kSimtRows;
+    for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
+        a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
+        const Seq* sq = seqs.data() + s0;
+        a.chunk = tc ? attend_chunk(c, sq, a.nseq, total) : INT32_MAX;
+        int64_t items = 0, split_tokens = 0, splits_max = 0;
+        for (int i = 0; i < a.nseq; ++i) {
+            const int64_t tiles = ((int64_t)sq[i].nq * c->G + rows - 1) / rows;
+            const int64_t splits = ((int64_t)sq[i].n + a.chunk - 1) / a.chunk;
+            a.brow[i] = sq[i].brow;
+            a.start[i] = sq[i].start;
+            a.nq[i] = sq[i].nq;
+            a.item0[i] = (int32_t)items;
+            a.comb0[i] = (int32_t)split_tokens;
+            items += tiles * splits * c->Hkv;
+            split_tokens += splits > 1 ? sq[i].nq : 0;
+            splits_max = std::max(splits_max, splits);
+        }
+        if (items > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
+        a.item0[a.nseq] = a.items = (int32_t)items;
+        a.comb0[a.nseq] = (int32_t)split_tokens;
+        a.part = c->d_logits;
+        a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
+        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (int)std::min<int64_t>(items, c->sm_count),
+                                              (cudaStream_t)stream)
+                           : launch_attend_simt(a, c->d, (cudaStream_t)stream);
         c->launches += 1;
+        if (e == cudaSuccess && split_tokens > 0) {
+            e = launch_attend_join(a, c->d, (cudaStream_t)stream);
+            c->launches += 1;
+        }
         if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");
     }
     return HIKV_OK;

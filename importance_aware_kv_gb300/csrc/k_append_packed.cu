@@ -11,17 +11,6 @@
 namespace hikv {
 namespace {
 
-// the sequence that packed row t belongs to
-__device__ __forceinline__ int32_t seq_of(const PackedSeqs& s, int32_t t) {
-    int32_t lo = 0, hi = s.n;
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (s.start[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // thread per (sequence, KV head): reserve the slots and map their pages
 __global__ void k_reserve_packed(const __grid_constant__ PackedAppendArgs a) {
     const int32_t i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -40,7 +29,7 @@ template <typename T>
 __global__ void __launch_bounds__(128) k_append_packed(const __grid_constant__ PackedAppendArgs a) {
     const View& v = a.v;
     const int32_t t = a.seqs.start[0] + blockIdx.x;
-    const int32_t b = seq_of(a.seqs, t);
+    const int32_t b = prefix_find(a.seqs.start, a.seqs.n, t);
     const int32_t u0 = a.u0 + (a.seqs.row0 + b) * v.hkv;
     const int32_t i = t - a.seqs.start[b], ntok = a.seqs.start[b + 1] - a.seqs.start[b];
     const int32_t half = a.rot / 2, pairs = v.d / 2;

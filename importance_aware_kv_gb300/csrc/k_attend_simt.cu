@@ -1,4 +1,4 @@
-// Causal attention of packed queries over the paged cache on the CUDA cores.
+// Causal attention of packed queries over the paged cache on the CUDA cores (fp32).
 //
 // One pass over the keys with a running maximum and sum per query row
 // (online softmax): with m the largest logit so far and l = sum 2^(t - m),
@@ -9,7 +9,6 @@
 // the group, so the G heads that share a KV head share its tiles -- against
 // tiles of 64 keys staged in shared memory as fp32; a thread forms 4 x 4
 // logits and 4 x D/16 outputs, all sums in fp32.
-#include "../../include/hikv.h"
 #include "hikv_internal.cuh"
 
 namespace hikv {
@@ -28,19 +27,7 @@ struct Simt {
     static constexpr int FLOATS = OFF_P + kBM * LP;
 };
 
-// 4 consecutive elements as fp32
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    float f[4];
-    Widen<__nv_bfloat16, 4>::run(*reinterpret_cast<const uint2*>(p), f);
-    return make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant__ AttendArgs a) {
     using C = Simt<D>;
     extern __shared__ float sm[];
@@ -50,18 +37,11 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
     float* Ps = sm + C::OFF_P;
     const View& v = a.v;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int32_t g = blockIdx.x % v.hkv, tile = blockIdx.x / v.hkv;
-    int32_t b = 0;
-    {
-        int32_t hi = a.seqs.n;
-        while (hi - b > 1) {
-            const int32_t mid = (b + hi) >> 1;
-            if (a.tile0[mid] <= tile) b = mid;
-            else hi = mid;
-        }
-    }
-    const int32_t u = a.u0 + (a.seqs.row0 + b) * v.hkv + g;
-    const int32_t nq = a.seqs.start[b + 1] - a.seqs.start[b];
+    const int32_t i0 = prefix_find(a.item0, a.nseq, blockIdx.x);
+    const int32_t nq = a.nq[i0], first = a.start[i0];
+    const int32_t g = (blockIdx.x - a.item0[i0]) % v.hkv;
+    const int32_t tile = (a.item0[i0 + 1] - 1 - (int32_t)blockIdx.x) / v.hkv;   // the last one first
+    const int32_t u = a.u0 + a.brow[i0] * v.hkv + g;
     const int32_t n = v.len[u];
     if (n < nq || n > v.cap) {
         if (tid == 0) atomicOr(v.err, DEVERR_STATE);
@@ -69,15 +49,15 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
     }
     const int32_t G = 1 << a.gshift;
     const int64_t rows = (int64_t)nq << a.gshift;
-    const int64_t r0 = (int64_t)(tile - a.tile0[b]) * kBM;
+    const int64_t r0 = (int64_t)tile * kBM;
     const int32_t seen0 = n - nq;   // slots before the first query's own
 
     for (int i = tid; i < kBM * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r0 + r < rows) {
-            const int32_t t = a.seqs.start[b] + (int32_t)((r0 + r) >> a.gshift), h = (g << a.gshift) + (int32_t)((r0 + r) & (G - 1));
-            x = load4(reinterpret_cast<const T*>(a.q.row(t, h)) + c);
+            const int32_t t = first + (int32_t)((r0 + r) >> a.gshift), h = (g << a.gshift) + (int32_t)((r0 + r) & (G - 1));
+            x = *reinterpret_cast<const float4*>(a.q.row(t, h) + 4 * c);
         }
         *reinterpret_cast<float4*>(Qs + r * C::LD + c) = x;
     }
@@ -105,8 +85,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
             if (s0 + r <= last_lim) {
                 const uint8_t* kp = row_ptr(v, u, s0 + r, false);
                 const uint8_t* vp = row_ptr(v, u, s0 + r, true);
-                if (kp) x = load4(reinterpret_cast<const T*>(kp) + c);
-                if (vp) y = load4(reinterpret_cast<const T*>(vp) + c);
+                if (kp) x = *reinterpret_cast<const float4*>(kp + 4 * c);
+                if (vp) y = *reinterpret_cast<const float4*>(vp + 4 * c);
             }
             *reinterpret_cast<float4*>(Ks + r * C::LD + c) = x;
             *reinterpret_cast<float4*>(Vs + r * D + c) = y;
@@ -183,31 +163,30 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
     for (int i = 0; i < 4; ++i) {
         const int64_t r = r0 + ty + 16 * i;
         if (r >= rows) continue;
-        const int32_t t = a.seqs.start[b] + (int32_t)(r >> a.gshift), h = (g << a.gshift) + (int32_t)(r & (G - 1));
-        T* dst = reinterpret_cast<T*>(a.out.row(t, h));
+        const int32_t t = first + (int32_t)(r >> a.gshift), h = (g << a.gshift) + (int32_t)(r & (G - 1));
+        float* dst = reinterpret_cast<float*>(a.out.row(t, h));
         const float inv = 1.0f / l[i];
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
-            store4(dst + tx * 4 + 64 * j,
-                   make_float4(o[i][j].x * inv, o[i][j].y * inv, o[i][j].z * inv, o[i][j].w * inv));
+            *reinterpret_cast<float4*>(dst + tx * 4 + 64 * j) =
+                make_float4(o[i][j].x * inv, o[i][j].y * inv, o[i][j].z * inv, o[i][j].w * inv);
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-    const void* f = (const void*)k_attend_simt<T, D>;
+    const void* f = (const void*)k_attend_simt<D>;
     const size_t smem = Simt<D>::FLOATS * sizeof(float);
     cudaError_t e = func_smem_optin(f, smem);
     if (e != cudaSuccess) return e;
-    k_attend_simt<T, D><<<a.items, kThreads, smem, s>>>(a);
+    k_attend_simt<D><<<a.items, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attend_simt(const AttendArgs& a, int dtype, int d, cudaStream_t s) {
-    if (dtype == HIKV_BF16) return d == 128 ? launch<__nv_bfloat16, 128>(a, s) : launch<__nv_bfloat16, 64>(a, s);
-    return d == 128 ? launch<float, 128>(a, s) : launch<float, 64>(a, s);
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s) {
+    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
 }
 
 }  // namespace hikv

@@ -1,0 +1,625 @@
+// Causal attention of packed queries over the paged cache on the tensor cores
+// (bf16), and the join of split results.
+//
+//   o_i = sum_{s <= lim_i} 2^(t_is - m_i) v_s / sum_{s <= lim_i} 2^(t_is - m_i),
+//   t_is = scale log2(e) q_i . k_s,
+//
+// in one pass over the keys.  The exponent's reference m_i is a running
+// maximum that moves only when a tile's maximum passes it by more than 8 (in
+// powers of two): until then 2^(t - m) <= 256, which fp32 sums and the bf16
+// probabilities hold without loss, and the accumulator needs no rescaling.
+//
+// A persistent CTA takes work items of 256 query rows x one KV head: two
+// tiles of 128 rows that share every key tile, so that the tensor cores work
+// on one while the softmax of the other runs.
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread a row: logits from
+//                   tensor memory, probabilities back over them as bf16
+//   warp 8          TMA: the query tiles, then K and V tiles of 128 keys
+//                   through a ring of stages (boxes of at most one page)
+//   warp 9          one thread issues the products: S = Q K^T (both operands in shared
+//                   memory), O += P V (P in tensor memory)
+//   warp 10         the V tiles at the end of what rows see: rows past the last
+//                   visible key become zero, non-finite values are
+//                   taken out and added back only for the rows that see them
+// Tensor memory: S/P of tile 0 and 1 in columns [0, 128) and [128, 256), O in
+// [256, 256 + D) and [384, 384 + D).  The products of one CTA execute in the
+// order they are issued -- O0 += P0 V(t), S0 = Q0 K(t+1), O1 += P1 V(t),
+// S1 = Q1 K(t+1) -- so S(t+1) lands after P(t) was read, and a tile's S being
+// complete means its O is up to date.
+//
+// Probabilities enter the product with V as bf16 (relative error 2^-8 each,
+// averaged over the keys); the sums l are of the fp32 values.
+#include "hikv_internal.cuh"
+
+namespace hikv {
+namespace {
+
+constexpr int kThreads = 352;
+constexpr int kKeys = kTcKeys, kRows = kTcRows;
+
+template <int D>
+struct Tc {
+    static constexpr int HALVES = D / 64;                 // 128-byte columns blocks of a row
+    static constexpr int BLOCK = 128 * 128;               // 128 rows x 128 bytes
+    static constexpr int TILE = HALVES * BLOCK;           // a tile of Q, K or V
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int OFF_Q = 0;                       // two tiles
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
+    // barriers: kv_full[STAGES], kv_empty[STAGES], v_ok[STAGES], q_full, q_empty, s_full[2], p_full[2], o_full[2],
+    // drained
+    static constexpr int NBAR = 3 * STAGES + 9;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory address, epilogue count, overlay item
+    static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
+    static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
+};
+
+// ---- tcgen05 ----
+// instruction descriptor: fp32 accumulator, bf16 A and B, A k-major; B
+// k-major or (trans) n-major
+constexpr uint32_t idesc_of(int M, int N, bool b_trans) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_trans ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+// shared-memory matrix descriptor, 128-byte swizzle: lbo between 64-element
+// blocks along the contiguous dimension, sbo between groups of eight rows
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// arrive on `bar` when every product this thread has issued is complete
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                 "=r"(r[i + 6]), "=r"(r[i + 7])
+#define RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                  "+r"(r[i + 6]), "+r"(r[i + 7])
+#define I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                 "r"(r[i + 6]), "r"(r[i + 7])
+// 32 columns of this thread's lane; the registers are valid after
+// tmem_wait_ld() and held() in front of their first use
+__device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
+        : "r"(addr));
+}
+__device__ __forceinline__ void held(uint32_t* r) {
+    asm volatile("" : RW8(r, 0), RW8(r, 8), RW8(r, 16), RW8(r, 24));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::I8(r, 0),
+        I8(r, 8), I8(r, 16), I8(r, 24), "r"(addr)
+        : "memory");
+}
+#undef R8
+#undef RW8
+#undef I8
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a bounded wait of a whole warp: all lanes agree on the outcome
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t index) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, kWaitAttend, index));
+}
+
+// A work item, the same in every warp
+struct Item {
+    int32_t u, g, rows, r0, first, seen0, lo, split;
+    int32_t nt[2], ntiles;   // key tiles of each row tile, and of the item
+    int32_t lim0;            // last slot that the item's first row sees
+    int32_t end;             // one past the last slot that any row sees in this split
+    bool split_out;
+};
+__device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item& w) {
+    const View& v = a.v;
+    const int32_t i = prefix_find(a.item0, a.nseq, it);
+    const int32_t nq = a.nq[i];
+    w.rows = nq << a.gshift;
+    const int32_t tiles = (w.rows + kRows - 1) / kRows;
+    const int32_t rem = it - a.item0[i], nsplit = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
+    w.g = rem % v.hkv;
+    const int32_t x = rem / v.hkv;
+    w.split = x % nsplit;
+    w.r0 = (tiles - 1 - x / nsplit) * kRows;
+    w.split_out = nsplit > 1;
+    w.first = a.start[i];
+    w.u = a.u0 + a.brow[i] * v.hkv + w.g;
+    const int32_t n = v.len[w.u];
+    if (n < nq || n > v.cap) {
+        if (threadIdx.x == 0) atomicOr(v.err, DEVERR_STATE);
+        return false;
+    }
+    w.seen0 = n - nq;
+    w.lim0 = w.seen0 + (w.r0 >> a.gshift);
+    w.lo = w.split_out ? w.split * a.chunk : 0;
+    w.end = 0;
+    w.ntiles = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int32_t a0 = w.r0 + 128 * t, a1 = min(a0 + 128, w.rows) - 1;
+        int32_t hi = a0 < w.rows ? w.seen0 + (a1 >> a.gshift) + 1 : 0;
+        if (w.split_out) hi = min(hi, w.lo + a.chunk);
+        w.nt[t] = hi > w.lo ? (hi - w.lo + kKeys - 1) / kKeys : 0;
+        w.end = max(w.end, hi);
+        w.ntiles = max(w.ntiles, w.nt[t]);
+    }
+    return w.ntiles > 0;
+}
+// tile t holds slots that the item's first row does not see, or that do not exist
+__device__ __forceinline__ bool edge_tile(const Item& w, int32_t t) { return w.lo + t * kKeys + kKeys - 1 > w.lim0; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kvmap) {
+    using C = Tc<D>;
+    extern __shared__ __align__(128) uint8_t raw[];
+    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+    uint64_t* kv_empty = kv_full + C::STAGES;
+    uint64_t* v_ok = kv_empty + C::STAGES;
+    uint64_t* q_full = v_ok + C::STAGES;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 2;
+    uint64_t* drained = o_full + 2;
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
+    int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
+    const View& v = a.v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 2);   // the products' completion and warp 10
+            mbar_init(&v_ok[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);     // one lane of each softmax warp
+            mbar_init(&o_full[i], 1);
+        }
+        misc[1] = 0;                      // epilogues done, in warps
+        misc[2] = 0xFFFFFFFFu;            // the item that `over` belongs to
+        fence_mbar_init();
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kvmap);
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(sm + C::OFF_MISC))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    if (warp < 8) {
+        // ---------------- softmax ----------------
+        const int tile = warp >> 2;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lane_base + 128 * tile, to = tmem + lane_base + 256 + 128 * tile;
+        uint32_t sphase = 0, ophase = 0;
+        const float c = a.qscale;
+        uint32_t count = 0;
+        bool ok = true;
+        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+            Item w;
+            if (!load_item(a, it, w)) continue;
+            const int32_t row = w.r0 + 128 * tile + 32 * (warp & 3) + lane;
+            const int32_t rc = min(row, w.rows - 1);
+            const int32_t lim = w.seen0 + (rc >> a.gshift);   // this row sees slots [0, lim]
+            const int32_t lim_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3), w.rows - 1) >> a.gshift);
+            float m = -INFINITY, l = 0.f;
+            for (int32_t t = 0; t < w.nt[tile]; ++t) {
+                if (!warp_wait(&s_full[tile], sphase, v.err, 0x100 + t)) { ok = false; break; }
+                sphase ^= 1;
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld32(s + 32 * j, ts + 32 * j);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) held(s + 32 * j);
+                const int32_t s0 = w.lo + t * kKeys;
+                if (s0 + kKeys - 1 > lim_w) {
+                    const int32_t left = lim - s0;   // columns [0, left] are seen
+#pragma unroll
+                    for (int j = 0; j < 128; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 128; j += 4) {
+                    mx0 = fmaxf(mx0, __uint_as_float(s[j]));
+                    mx1 = fmaxf(mx1, __uint_as_float(s[j + 1]));
+                    mx2 = fmaxf(mx2, __uint_as_float(s[j + 2]));
+                    mx3 = fmaxf(mx3, __uint_as_float(s[j + 3]));
+                }
+                const float mt = fmaxf(m, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)));
+                // (mt - m is NaN while both are -inf: no move)
+                const bool move = (mt - m) * c > 8.0f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = m == mt ? 1.f : ex2((m - mt) * c);
+                    if (t > 0) {
+#pragma unroll
+                        for (int j = 0; j < D; j += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o, to + j);
+                            tmem_wait_ld();
+                            held(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(to + j, o);
+                        }
+                    }
+                    l *= f;
+                    m = mt;
+                }
+                const float base = m == -INFINITY ? 0.f : m * c;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                float2 sum = make_float2(0.f, 0.f);
+                uint32_t p[64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
+                    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                    sum.x += e.x;
+                    sum.y += e.y;
+                    p[j] = pack_bf16x2(e.x, e.y);
+                }
+                l += sum.x + sum.y;
+                tmem_st32(ts, p);
+                tmem_st32(ts + 32, p + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[tile]);
+            }
+            if (!ok) break;
+            if (w.nt[tile] > 0) {
+                if (!warp_wait(&o_full[tile], ophase, v.err, 0x200)) { ok = false; break; }
+                ophase ^= 1;
+                tc_fence_after();
+                const int32_t tok = w.first + (row >> a.gshift);
+                const int32_t h = (w.g << a.gshift) + (row & ((1 << a.gshift) - 1));
+                const bool over_here = misc[2] == (uint32_t)it;
+                const float inv = w.split_out ? 1.f : 1.0f / l;
+                const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h;
+#pragma unroll
+                for (int j = 0; j < D; j += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o, to + j);
+                    tmem_wait_ld();
+                    held(o);
+                    if (over_here) {
+                        // non-finite values of the edge tiles, for the rows that see them
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float x = __uint_as_float(o[i]);
+                            if (over[j + i] <= lim) x += INFINITY;
+                            if (over[D + j + i] <= lim) x -= INFINITY;
+                            if (over[2 * D + j + i] <= lim) x = __int_as_float(0x7FC00000);
+                            o[i] = __float_as_uint(x);
+                        }
+                    }
+                    if (row < w.rows) {
+                        if (w.split_out) {
+                            float4* dst = reinterpret_cast<float4*>(a.part + pr * D + j);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(a.out.row(tok, h) + 2 * j);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    x[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                                       __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                                dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                    }
+                }
+                if (w.split_out && row < w.rows)
+                    *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
+            }
+            ++count;
+            __syncwarp();
+            if (lane == 0) atomicAdd(const_cast<uint32_t*>(&misc[1]), 1u);
+        }
+    } else if (warp == 8) {
+        // ---------------- TMA ----------------
+        const int bx = min(v.page_tokens, 128), nb = 128 / bx;   // rows of a box, boxes of a tile
+        uint32_t fill = 0, items = 0;
+        bool ok = true;
+        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+            Item w;
+            if (!load_item(a, it, w)) continue;
+            if (items > 0 && !warp_wait(q_empty, (items - 1) & 1, v.err, 0x300)) { ok = false; break; }
+            ++items;
+            if (lane == 0) {
+                const int tiles = w.r0 + 128 < w.rows ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, tiles * C::TILE);
+                for (int t = 0; t < tiles; ++t)
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                        tma_load_3d(sm + C::OFF_Q + t * C::TILE + hf * C::BLOCK, &qmap, 64 * hf, w.g << a.gshift,
+                                    w.first + ((w.r0 + 128 * t) >> a.gshift), q_full);
+            }
+            for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
+                const int st = fill % C::STAGES;
+                const uint32_t use = fill / C::STAGES;
+                if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, v.err, 0x400 + st)) { ok = false; break; }
+                const bool is_v = x & 1;
+                const int32_t s0 = w.lo + (x >> 1) * kKeys;
+                // lane -> (box, half); a box wholly past the last visible slot is not loaded
+                const int box = lane / C::HALVES, hf = lane % C::HALVES;
+                const int32_t s = s0 + box * bx;
+                int32_t pg = -1;
+                if (box < nb && s < w.end) {
+                    pg = unit_page(v, w.u, s);
+                    if (pg < 0 || pg >= v.pool_pages) {
+                        atomicOr(v.err, DEVERR_PAGE);
+                        pg = -1;
+                    }
+                }
+                const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], cnt * bx * 128);
+                __syncwarp();
+                if (pg >= 0)
+                    tma_load_2d(sm + C::OFF_KV + st * C::TILE + hf * C::BLOCK + box * bx * 128, &kvmap, 64 * hf,
+                                (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens + (s & (v.page_tokens - 1))),
+                                &kv_full[st]);
+            }
+        }
+        // every copy has landed and every commit arrived before the CTA ends
+        if (ok && items > 0) warp_wait(q_empty, (items - 1) & 1, v.err, 0x301);
+        for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f) {
+            const int st = f % C::STAGES;
+            const uint32_t par = (f / C::STAGES) & 1;
+            if (ok) warp_wait(&kv_empty[st], par, v.err, 0x401);
+            else warp_wait(&kv_full[st], par, v.err, 0x402);
+        }
+        if (!ok && items > 0) warp_wait(q_full, (items - 1) & 1, v.err, 0x302);
+    } else if (warp == 9) {
+        // ---------------- products ----------------
+        constexpr uint32_t id_qk = idesc_of(128, kKeys, false), id_pv = idesc_of(128, D, true);
+        const uint32_t sq = smem_u32(sm + C::OFF_Q), skv = smem_u32(sm + C::OFF_KV);
+        uint32_t fill = 0, items = 0, pphase[2] = {0, 0}, vuse = 0;
+        bool ok = true;
+        auto full = [&](uint32_t f) {
+            return warp_wait(&kv_full[f % C::STAGES], (f / C::STAGES) & 1, v.err, 0x500);
+        };
+        auto qk = [&](int tile, uint32_t f) {   // S_tile = Q_tile K^T
+            const uint32_t k = skv + (f % C::STAGES) * C::TILE, q = sq + tile * C::TILE;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = (i / 4) * C::BLOCK + (i % 4) * 32;
+                    mma_ss(tmem + 128 * tile, sdesc(q + off, 16, 1024), sdesc(k + off, 16, 1024), id_qk, i > 0);
+                }
+                mma_commit(&s_full[tile]);
+            }
+        };
+        auto pv = [&](int tile, uint32_t f, bool first, bool last) {   // O_tile += P_tile V
+            const uint32_t b = skv + (f % C::STAGES) * C::TILE;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                    mma_ts(tmem + 256 + 128 * tile, tmem + 128 * tile + 8 * i, sdesc(b + i * 2048, C::BLOCK, 1024), id_pv,
+                           !(first && i == 0));
+                if (last) mma_commit(&o_full[tile]);
+            }
+        };
+        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+            Item w;
+            if (!load_item(a, it, w)) continue;
+            ok = warp_wait(q_full, items & 1, v.err, 0x501) && full(fill);
+            if (!ok) break;
+            ++items;
+            tc_fence_after();
+            for (int i = 0; i < 2; ++i)
+                if (w.nt[i] > 0) qk(i, fill);
+            if (lane == 0) {
+                mma_commit(&kv_empty[fill % C::STAGES]);
+                if (w.ntiles == 1) mma_commit(q_empty);
+            }
+            for (int32_t t = 0; ok && t < w.ntiles; ++t, fill += 2) {
+                const uint32_t fv = fill + 1, fk = fill + 2;   // V(t), K(t + 1)
+                const bool more = t + 1 < w.ntiles;
+                ok = full(fv);
+                if (ok && edge_tile(w, t)) {
+                    const int st = fv % C::STAGES;
+                    ok = warp_wait(&v_ok[st], (vuse >> st) & 1, v.err, 0x502);
+                    vuse ^= 1u << st;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (ok && t < w.nt[i]) {
+                        ok = warp_wait(&p_full[i], pphase[i], v.err, 0x503);
+                        pphase[i] ^= 1;
+                        tc_fence_after();
+                        if (ok) pv(i, fv, t == 0, t + 1 == w.nt[i]);
+                    }
+                    if (i == 0 && ok && more) ok = full(fk);
+                    if (i == 1 && ok && lane == 0) mma_commit(&kv_empty[fv % C::STAGES]);
+                    if (ok && t + 1 < w.nt[i]) qk(i, fk);
+                }
+                if (ok && more && lane == 0) {
+                    mma_commit(&kv_empty[fk % C::STAGES]);
+                    if (t + 2 == w.ntiles) mma_commit(q_empty);
+                }
+                __syncwarp();
+            }
+        }
+        // nothing is in flight when the CTA ends, after a wait that gave up neither
+        if (lane == 0) mma_commit(drained);
+        warp_wait(drained, 0, v.err, 0x504);
+    } else {
+        // ---------------- the edge of what rows see ----------------
+        uint32_t fill = 0, seen = 0;
+        bool ok = true;
+        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+            Item w;
+            if (!load_item(a, it, w)) continue;
+            for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
+                const int st = fill % C::STAGES;
+                ok = warp_wait(&kv_full[st], (fill / C::STAGES) & 1, v.err, 0x600);
+                if (!ok) break;
+                if ((x & 1) && edge_tile(w, x >> 1)) {
+                    const int32_t s0 = w.lo + (x >> 1) * kKeys;
+                    const int32_t rv = min(kKeys, w.end - s0);   // rows that hold visible tokens
+                    uint8_t* tile = sm + C::OFF_KV + st * C::TILE;
+                    uint32_t top = 0;   // largest magnitude in either half of the words
+                    for (int hf = 0; hf < C::HALVES; ++hf) {
+                        uint4* p = reinterpret_cast<uint4*>(tile + hf * C::BLOCK);
+#pragma unroll 8
+                        for (int i = lane; i < rv * 8; i += 32) {
+                            const uint4 y = p[i];
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                                         __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu)));
+                        }
+                        for (int i = rv * 8 + lane; i < kKeys * 8; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
+                    if (__any_sync(0xffffffffu, bad)) {
+                        if (misc[2] != (uint32_t)it) {
+                            // `over` is free once every epilogue before this item has read it
+                            const uint64_t t0 = global_ns();
+                            while (misc[1] < 8 * seen) {
+                                if (global_ns() - t0 > kWaitLimitNs) {
+                                    record_timeout(v.err, kWaitAttend, 0x601, global_ns() - t0);
+                                    ok = false;
+                                    break;
+                                }
+                            }
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            for (int i = lane; i < 3 * D; i += 32) over[i] = 0x7FFFFFFF;
+                            __syncwarp();
+                        }
+                        for (int hf = 0; hf < C::HALVES; ++hf)
+                            for (int i = lane; i < rv * 64; i += 32) {
+                                uint16_t* e = reinterpret_cast<uint16_t*>(tile + hf * C::BLOCK) + i;
+                                const uint16_t y = *e;
+                                if ((y & 0x7F80) != 0x7F80) continue;
+                                const int r = i >> 6, col = 64 * hf + ((((i >> 3) & 7) ^ (r & 7)) << 3) + (i & 7);
+                                const int kind = (y & 0x7F) ? 2 : (y >> 15);
+                                atomicMin(&over[kind * D + col], s0 + r);
+                                *e = 0;
+                            }
+                        __syncwarp();
+                        __threadfence_block();
+                        if (lane == 0) misc[2] = (uint32_t)it;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_ok[st]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_empty[st]);
+            }
+            ++seen;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Join the splits of every query row: warp per row (t, h) of the sequences
+// whose keys were split.  With m the largest of the partial maxima,
+// o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+template <int D>
+__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a) {
+    const View& v = a.v;
+    const int32_t x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int32_t tok = x / v.hq, h = x % v.hq;
+    if (tok >= a.comb0[a.nseq]) return;
+    const int32_t i = prefix_find(a.comb0, a.nseq, tok);
+    const int32_t j = tok - a.comb0[i];
+    const int32_t n = v.len[a.u0 + a.brow[i] * v.hkv + (h >> a.gshift)];
+    const int32_t lim = n - a.nq[i] + j;
+    if (lim < 0 || n > v.cap) return;
+    const int32_t ns = lim / a.chunk + 1;
+    const int64_t row = (int64_t)(a.start[i] + j) * v.hq + h;
+    float m = -INFINITY;
+    for (int32_t s = 0; s < ns; ++s) m = fmaxf(m, a.part_ml[(s * a.part_rows + row) * 2]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[D / 32] = {};
+    for (int32_t s = 0; s < ns; ++s) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * a.part_rows + row) * 2);
+        const float f = exp2f(ml.x - base);
+        l = fmaf(f, ml.y, l);
+        const float* p = a.part + (s * a.part_rows + row) * D + lane * (D / 32);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) o[k] = fmaf(f, p[k], o[k]);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out.row(a.start[i] + j, h)) + lane * (D / 64);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) dst[k] = pack_bf16x2(o[2 * k] / l, o[2 * k + 1] / l);
+}
+
+template <int D>
+cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int n_ctas, cudaStream_t s) {
+    const void* f = (const void*)k_attend_tc<D>;
+    cudaError_t e = func_smem_optin(f, Tc<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    k_attend_tc<D><<<n_ctas, kThreads, Tc<D>::BYTES, s>>>(a, qmap, kvmap);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
+                             int n_ctas, cudaStream_t s) {
+    return d == 128 ? launch<128>(a, qmap, kvmap, n_ctas, s) : launch<64>(a, qmap, kvmap, n_ctas, s);
+}
+
+cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s) {
+    const int32_t grid = (int32_t)(((int64_t)a.comb0[a.nseq] * a.v.hq + 3) / 4);
+    if (d == 128) k_attend_join<128><<<grid, 128, 0, s>>>(a);
+    else k_attend_join<64><<<grid, 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace hikv
