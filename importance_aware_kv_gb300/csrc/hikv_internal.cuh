@@ -376,6 +376,15 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+// packed fp32 pair addition
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+    return d;
+}
+
 // 1-D bulk copy global -> shared (TMA engine), completion counted on `bar`.
 // dst, src 16-byte aligned; bytes a multiple of 16.
 // mma.sync m16n8k16, bf16 operands, fp32 accumulate: D = A * B + D with A

@@ -34,7 +34,11 @@
 namespace hikv {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;   // warp 11 only keeps the last four a warpgroup
+// Registers a thread: 168 at launch (384 x 168 of the SM's 64 K); the softmax
+// warps, which hold a row of 128 logits each, take what the others give up:
+// 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kKeys = kTcKeys, kRows = kTcRows;
 
 template <int D>
@@ -108,6 +112,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t addr) {
 }
 __device__ __forceinline__ void held(uint32_t* r) {
     asm volatile("" : RW8(r, 0), RW8(r, 8), RW8(r, 16), RW8(r, 24));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15};" ::I8(r, 0),
+        I8(r, 8), "r"(addr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
     asm volatile(
@@ -230,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ---------------- softmax ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int tile = warp >> 2;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lane_base + 128 * tile, to = tmem + lane_base + 256 + 128 * tile;
@@ -292,18 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float base = m == -INFINITY ? 0.f : m * c;
                 const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
                 float2 sum = make_float2(0.f, 0.f);
-                uint32_t p[64];
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
-                    const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                    sum.x += e.x;
-                    sum.y += e.y;
-                    p[j] = pack_bf16x2(e.x, e.y);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t* y = s + 32 * k + 2 * j;
+                        const float2 x = ffma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, b2);
+                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                        sum = fadd2(sum, e);
+                        p[j] = pack_bf16x2(e.x, e.y);
+                    }
+                    tmem_st16(ts + 16 * k, p);
                 }
                 l += sum.x + sum.y;
-                tmem_st32(ts, p);
-                tmem_st32(ts + 32, p + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -364,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) atomicAdd(const_cast<uint32_t*>(&misc[1]), 1u);
         }
-    } else if (warp == 8) {
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {
         // ---------------- TMA ----------------
         const int bx = min(v.page_tokens, 128), nb = 128 / bx;   // rows of a box, boxes of a tile
         uint32_t fill = 0, items = 0;
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // nothing is in flight when the CTA ends, after a wait that gave up neither
         if (lane == 0) mma_commit(drained);
         warp_wait(drained, 0, v.err, 0x504);
-    } else {
+    } else if (warp == 10) {
         // ---------------- the edge of what rows see ----------------
         uint32_t fill = 0, seen = 0;
         bool ok = true;
@@ -557,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++seen;
         }
+    }
     }
     tc_fence_before();
     __syncthreads();
