@@ -16,16 +16,16 @@
 //                   tensor memory, probabilities back over them as bf16
 //   warp 8          TMA: the query tiles, then K and V tiles of 128 keys
 //                   through a ring of stages (boxes of at most one page)
-//   warp 9          one thread issues the products: S = Q K^T (both operands in shared
-//                   memory), O += P V (P in tensor memory)
+//   warps 9, 11     one thread each issues the products of row tile 0 and 1: S = Q K^T
+//                   (both operands in shared memory), O += P V (P in tensor memory)
 //   warp 10         the V tiles at the end of what rows see: rows past the last
 //                   visible key become zero, non-finite values are
 //                   taken out and added back only for the rows that see them
 // Tensor memory: S/P of tile 0 and 1 in columns [0, 128) and [128, 256), O in
-// [256, 256 + D) and [384, 384 + D).  The products of one CTA execute in the
-// order they are issued -- O0 += P0 V(t), S0 = Q0 K(t+1), O1 += P1 V(t),
-// S1 = Q1 K(t+1) -- so S(t+1) lands after P(t) was read, and a tile's S being
-// complete means its O is up to date.
+// [256, 256 + D) and [384, 384 + D).  The products of one thread execute in
+// the order they are issued -- O += P V(t), S = Q K(t+1) -- so S(t+1) lands
+// after P(t) was read, and a tile's S being complete means its O is up to
+// date.
 //
 // Probabilities enter the product with V as bf16 (relative error 2^-8 each,
 // averaged over the keys); the sums l are of the fp32 values.
@@ -34,7 +34,7 @@
 namespace hikv {
 namespace {
 
-constexpr int kThreads = 384;   // warp 11 only keeps the last four a warpgroup
+constexpr int kThreads = 384;
 // Registers a thread: 168 at launch (384 x 168 of the SM's 64 K); the softmax
 // warps, which hold a row of 128 logits each, take what the others give up:
 // 256 x 208 + 128 x 88 = 384 x 168.
@@ -136,9 +136,32 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+// position in a ring of N stages and the parity of its fill
+template <int N>
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
 // a bounded wait of a whole warp: all lanes agree on the outcome
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t index) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, kWaitAttend, index));
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
 }
 
 // A work item, the same in every warp
@@ -211,12 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 2);   // the products' completion and warp 10
+            mbar_init(&kv_empty[i], 3);   // both tiles' products are complete, and warp 10
             mbar_init(&v_ok[i], 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
-        mbar_init(drained, 1);
+        mbar_init(q_empty, 2);
+        mbar_init(drained, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);     // one lane of each softmax warp
@@ -273,15 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 128; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
                 }
-                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                float mx[4] = {m, m, m, m};
 #pragma unroll
-                for (int j = 0; j < 128; j += 4) {
-                    mx0 = fmaxf(mx0, __uint_as_float(s[j]));
-                    mx1 = fmaxf(mx1, __uint_as_float(s[j + 1]));
-                    mx2 = fmaxf(mx2, __uint_as_float(s[j + 2]));
-                    mx3 = fmaxf(mx3, __uint_as_float(s[j + 3]));
-                }
-                const float mt = fmaxf(m, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)));
+                for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
+                const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 // (mt - m is NaN while both are -inf: no move)
                 const bool move = (mt - m) * c > 8.0f;
                 if (__any_sync(0xffffffffu, move)) {
@@ -433,80 +454,89 @@ __global__ void __launch_bounds__(kThreads, 1)
             else warp_wait(&kv_full[st], par, v.err, 0x402);
         }
         if (!ok && items > 0) warp_wait(q_full, (items - 1) & 1, v.err, 0x302);
-    } else if (warp == 9) {
-        // ---------------- products ----------------
-        constexpr uint32_t id_qk = idesc_of(128, kKeys, false), id_pv = idesc_of(128, D, true);
-        const uint32_t sq = smem_u32(sm + C::OFF_Q), skv = smem_u32(sm + C::OFF_KV);
-        uint32_t fill = 0, items = 0, pphase[2] = {0, 0}, vuse = 0;
-        bool ok = true;
-        auto full = [&](uint32_t f) {
-            return warp_wait(&kv_full[f % C::STAGES], (f / C::STAGES) & 1, v.err, 0x500);
-        };
-        auto qk = [&](int tile, uint32_t f) {   // S_tile = Q_tile K^T
-            const uint32_t k = skv + (f % C::STAGES) * C::TILE, q = sq + tile * C::TILE;
-            if (lane == 0) {
+    } else if (warp == 9 || warp == 11) {
+        // ---------------- products of row tile 0 (warp 9) and 1 (warp 11) ----------------
+        // One thread each.  What it waits for besides P it waits for while
+        // products it has issued are still running, and the next item is read
+        // early: about four products queue, so a late issue is idle time.
+        if (elect_one()) {
+            constexpr uint32_t id_qk = idesc_of(128, kKeys, false), id_pv = idesc_of(128, D, true);
+            const int tile = warp == 9 ? 0 : 1;
+            const uint64_t dq = sdesc(smem_u32(sm + C::OFF_Q + tile * C::TILE), 16, 1024);
+            const uint64_t dk = sdesc(smem_u32(sm + C::OFF_KV), 16, 1024), dv = sdesc(smem_u32(sm + C::OFF_KV), C::BLOCK, 1024);
+            const uint32_t ts = tmem + 128 * tile, to = tmem + 256 + 128 * tile;
+            uint32_t qphase = 0, pphase = 0, vuse = 0;
+            Ring<C::STAGES> r;   // the fill in turn
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t index) {
+                ok = ok && mbar_wait_bounded(bar, parity, v.err, kWaitAttend, index);
+            };
+            auto qk = [&](int st) {   // S = Q K^T
+                const uint64_t k = dk + st * (C::TILE >> 4);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = (i / 4) * C::BLOCK + (i % 4) * 32;
-                    mma_ss(tmem + 128 * tile, sdesc(q + off, 16, 1024), sdesc(k + off, 16, 1024), id_qk, i > 0);
+                    const uint32_t off = ((i / 4) * C::BLOCK + (i % 4) * 32) >> 4;
+                    mma_ss(ts, dq + off, k + off, id_qk, i > 0);
                 }
                 mma_commit(&s_full[tile]);
-            }
-        };
-        auto pv = [&](int tile, uint32_t f, bool first, bool last) {   // O_tile += P_tile V
-            const uint32_t b = skv + (f % C::STAGES) * C::TILE;
-            if (lane == 0) {
+            };
+            auto pv = [&](int st, bool first) {   // O += P V
+                const uint64_t b = dv + st * (C::TILE >> 4);
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    mma_ts(tmem + 256 + 128 * tile, tmem + 128 * tile + 8 * i, sdesc(b + i * 2048, C::BLOCK, 1024), id_pv,
-                           !(first && i == 0));
-                if (last) mma_commit(&o_full[tile]);
-            }
-        };
-        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-            Item w;
-            if (!load_item(a, it, w)) continue;
-            ok = warp_wait(q_full, items & 1, v.err, 0x501) && full(fill);
-            if (!ok) break;
-            ++items;
-            tc_fence_after();
-            for (int i = 0; i < 2; ++i)
-                if (w.nt[i] > 0) qk(i, fill);
-            if (lane == 0) {
-                mma_commit(&kv_empty[fill % C::STAGES]);
+                for (int i = 0; i < kKeys / 16; ++i) mma_ts(to, ts + 8 * i, b + i * (2048 >> 4), id_pv, !(first && i == 0));
+            };
+            Item w, next;
+            bool have = false;
+            int32_t it = blockIdx.x;
+            for (; it < a.items && !(have = load_item(a, it, w)); it += gridDim.x) {}
+            while (have) {
+                const int32_t nt = w.nt[tile];
+                wait(q_full, qphase, 0x501);
+                qphase ^= 1;
+                wait(&kv_full[r.st], r.ph, 0x500);
+                if (!ok) break;
+                tc_fence_after();
+                if (nt > 0) qk(r.st);
+                mma_commit(&kv_empty[r.st]);
                 if (w.ntiles == 1) mma_commit(q_empty);
-            }
-            for (int32_t t = 0; ok && t < w.ntiles; ++t, fill += 2) {
-                const uint32_t fv = fill + 1, fk = fill + 2;   // V(t), K(t + 1)
-                const bool more = t + 1 < w.ntiles;
-                ok = full(fv);
-                if (ok && edge_tile(w, t)) {
-                    const int st = fv % C::STAGES;
-                    ok = warp_wait(&v_ok[st], (vuse >> st) & 1, v.err, 0x502);
-                    vuse ^= 1u << st;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (ok && t < w.nt[i]) {
-                        ok = warp_wait(&p_full[i], pphase[i], v.err, 0x503);
-                        pphase[i] ^= 1;
-                        tc_fence_after();
-                        if (ok) pv(i, fv, t == 0, t + 1 == w.nt[i]);
+                r.step();
+                have = false;
+                for (it += gridDim.x; it < a.items && !(have = load_item(a, it, next)); it += gridDim.x) {}
+                for (int32_t t = 0; t < w.ntiles; ++t) {
+                    const bool more = t + 1 < w.ntiles;
+                    const int sv = r.st;   // V(t)
+                    wait(&kv_full[sv], r.ph, 0x505);
+                    if (edge_tile(w, t)) {
+                        wait(&v_ok[sv], (vuse >> sv) & 1, 0x502);
+                        vuse ^= 1u << sv;
                     }
-                    if (i == 0 && ok && more) ok = full(fk);
-                    if (i == 1 && ok && lane == 0) mma_commit(&kv_empty[fv % C::STAGES]);
-                    if (ok && t + 1 < w.nt[i]) qk(i, fk);
+                    r.step();
+                    if (more) wait(&kv_full[r.st], r.ph, 0x506);   // K(t + 1)
+                    if (t < nt) {
+                        wait(&p_full[tile], pphase, 0x503);
+                        pphase ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(sv, t == 0);
+                        if (t + 1 < nt) qk(r.st);
+                        else mma_commit(&o_full[tile]);
+                    }
+                    if (!ok) break;
+                    mma_commit(&kv_empty[sv]);
+                    if (more) {
+                        mma_commit(&kv_empty[r.st]);
+                        if (t + 2 == w.ntiles) mma_commit(q_empty);
+                        r.step();
+                    }
                 }
-                if (ok && more && lane == 0) {
-                    mma_commit(&kv_empty[fk % C::STAGES]);
-                    if (t + 2 == w.ntiles) mma_commit(q_empty);
-                }
-                __syncwarp();
+                if (!ok) break;
+                w = next;
             }
+            // nothing is in flight when the CTA ends, after a wait that gave up neither
+            mma_commit(drained);
+            mbar_wait_bounded(drained, 0, v.err, kWaitAttend, 0x504);
         }
-        // nothing is in flight when the CTA ends, after a wait that gave up neither
-        if (lane == 0) mma_commit(drained);
-        warp_wait(drained, 0, v.err, 0x504);
+        __syncwarp();
     } else if (warp == 10) {
         // ---------------- the edge of what rows see ----------------
         uint32_t fill = 0, seen = 0;
