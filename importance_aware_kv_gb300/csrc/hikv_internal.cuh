@@ -654,7 +654,7 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s);
 constexpr int kSimtRows = 64;   // query rows of a work item of that kernel
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
-                             int n_ctas, cudaStream_t s);
+                             cudaStream_t s);
 constexpr int kTcRows = 256;    // of the tensor-core kernel
 constexpr int kTcKeys = 128;    // keys per tile
 cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s);

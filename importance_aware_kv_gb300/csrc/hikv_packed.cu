@@ -273,8 +273,7 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
         a.comb0[a.nseq] = (int32_t)split_tokens;
         a.part = c->d_logits;
         a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
-        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (int)std::min<int64_t>(items, c->sm_count),
-                                              (cudaStream_t)stream)
+        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
                            : launch_attend_simt(a, c->d, (cudaStream_t)stream);
         c->launches += 1;
         if (e == cudaSuccess && split_tokens > 0) {

@@ -9,7 +9,7 @@
 // powers of two): until then 2^(t - m) <= 256, which fp32 sums and the bf16
 // probabilities hold without loss, and the accumulator needs no rescaling.
 //
-// A persistent CTA takes work items of 256 query rows x one KV head: two
+// A CTA takes one work item after the other, 256 query rows x one KV head: two
 // tiles of 128 rows that share every key tile, so that the tensor cores work
 // on one while the softmax of the other runs.
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread a row: logits from
@@ -51,9 +51,10 @@ struct Tc {
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
     // barriers: kv_full[STAGES], kv_empty[STAGES], v_ok[STAGES], q_full, q_empty, s_full[2], p_full[2], o_full[2],
-    // drained
-    static constexpr int NBAR = 3 * STAGES + 9;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory address, epilogue count, overlay item
+    // drained, next_full[2], next_empty[2]
+    static constexpr int NBAR = 3 * STAGES + 13;
+    static constexpr int OFF_NEXT = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // two answers of the work distributor
+    static constexpr int OFF_MISC = OFF_NEXT + 32;        // tensor memory address, epilogue count, overlay item, error
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -210,6 +211,66 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item&
 // tile t holds slots that the item's first row does not see, or that do not exist
 __device__ __forceinline__ bool edge_tile(const Item& w, int32_t t) { return w.lo + t * kKeys + kKeys - 1 > w.lim0; }
 
+// The work items after the CTA's first.  The grid has a CTA per item; a CTA
+// that has started takes the numbers of CTAs that have not, so the items go
+// out one by one, in order, to whoever is free.  Warp 8 asks for one item
+// ahead (ask()), every role reads the answer (take()); two answers are kept.
+constexpr int kReaders = 12;   // softmax warps, warps 8 and 10, both issuing threads
+struct NextItem {
+    uint64_t* full;
+    uint64_t* empty;
+    uint32_t addr;
+    uint32_t* err;
+    uint32_t k = 1;   // number of the item in question, from the CTA's first on
+    __device__ __forceinline__ int slot() const { return k & 1; }
+    __device__ __forceinline__ uint32_t parity() const { return ((k - 1) >> 1) & 1; }
+    // one thread of warp 8, once an item, until an answer was -1
+    __device__ __forceinline__ bool ask(uint32_t n) {
+        const int s = n & 1;
+        if (n > 2 && !mbar_wait_bounded(&empty[s], ((n - 3) >> 1) & 1, err, kWaitAttend, 0x700)) return false;
+        mbar_arrive_expect_tx(&full[s], 16);
+        asm volatile(
+            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                addr + 16 * s),
+            "r"(smem_u32(&full[s]))
+            : "memory");
+        return true;
+    }
+    __device__ __forceinline__ int32_t read() const {
+        uint32_t ok, x;
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+            "ld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(ok), "=r"(x)
+            : "r"(addr + 16 * slot())
+            : "memory");
+        fence_proxy_async_smem();
+        return ok ? (int32_t)x : -1;
+    }
+    // the next item or -1; a whole warp
+    __device__ __forceinline__ int32_t take(bool& good) {
+        good = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot()], parity(), err, kWaitAttend, 0x701));
+        if (!good) return -1;
+        const int32_t it = read();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot()]);
+        ++k;
+        return it;
+    }
+    // the same for one thread
+    __device__ __forceinline__ int32_t take_one(bool& good) {
+        good = good && mbar_wait_bounded(&full[slot()], parity(), err, kWaitAttend, 0x702);
+        if (!good) return -1;
+        const int32_t it = read();
+        mbar_arrive(&empty[slot()]);
+        ++k;
+        return it;
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -226,6 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* p_full = s_full + 2;
     uint64_t* o_full = p_full + 2;
     uint64_t* drained = o_full + 2;
+    uint64_t* next_full = drained + 1;
+    uint64_t* next_empty = next_full + 2;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
     int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
     const View& v = a.v;
@@ -244,9 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);     // one lane of each softmax warp
             mbar_init(&o_full[i], 1);
+            mbar_init(&next_full[i], 1);
+            mbar_init(&next_empty[i], kReaders);
         }
         misc[1] = 0;                      // epilogues done, in warps
         misc[2] = 0xFFFFFFFFu;            // the item that `over` belongs to
+        misc[3] = *reinterpret_cast<volatile uint32_t*>(v.err) & DEVERR_TIMEOUT;   // a wait gave up: start nothing more
         fence_mbar_init();
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kvmap);
@@ -261,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
+    const int32_t it0 = misc[3] ? -1 : (int32_t)blockIdx.x;   // -1: no item (left)
+    NextItem nx{next_full, next_empty, smem_u32(sm + C::OFF_NEXT), v.err};
 
     if (warp < 8) {
         // ---------------- softmax ----------------
@@ -270,9 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lane_base + 128 * tile, to = tmem + lane_base + 256 + 128 * tile;
         uint32_t sphase = 0, ophase = 0;
         const float c = a.qscale;
-        uint32_t count = 0;
         bool ok = true;
-        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
             Item w;
             if (!load_item(a, it, w)) continue;
             const int32_t row = w.r0 + 128 * tile + 32 * (warp & 3) + lane;
@@ -395,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.split_out && row < w.rows)
                     *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
             }
-            ++count;
             __syncwarp();
             if (lane == 0) atomicAdd(const_cast<uint32_t*>(&misc[1]), 1u);
         }
@@ -404,11 +470,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         // ---------------- TMA ----------------
         const int bx = min(v.page_tokens, 128), nb = 128 / bx;   // rows of a box, boxes of a tile
-        uint32_t fill = 0, items = 0;
+        uint32_t fill = 0, items = 0, asked = 0;
         bool ok = true;
-        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
             Item w;
-            if (!load_item(a, it, w)) continue;
+            const bool some = load_item(a, it, w);
+            ok = true;
+            if (lane == 0) ok = nx.ask(nx.k);
+            ++asked;
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            if (!ok) break;
+            if (!some) continue;
             if (items > 0 && !warp_wait(q_empty, (items - 1) & 1, v.err, 0x300)) { ok = false; break; }
             ++items;
             if (lane == 0) {
@@ -445,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 &kv_full[st]);
             }
         }
-        // every copy has landed and every commit arrived before the CTA ends
+        // every answer and copy has landed and every commit arrived before the CTA ends
+        if (!ok && asked >= nx.k) nx.take(ok), ok = false;
         if (ok && items > 0) warp_wait(q_empty, (items - 1) & 1, v.err, 0x301);
         for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f) {
             const int st = f % C::STAGES;
@@ -487,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             Item w, next;
             bool have = false;
-            int32_t it = blockIdx.x;
-            for (; it < a.items && !(have = load_item(a, it, w)); it += gridDim.x) {}
+            int32_t it = it0;
+            for (; it >= 0 && !(have = load_item(a, it, w)); it = nx.take_one(ok)) {}
             while (have) {
                 const int32_t nt = w.nt[tile];
                 wait(q_full, qphase, 0x501);
@@ -501,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.ntiles == 1) mma_commit(q_empty);
                 r.step();
                 have = false;
-                for (it += gridDim.x; it < a.items && !(have = load_item(a, it, next)); it += gridDim.x) {}
+                while ((it = nx.take_one(ok)) >= 0 && !(have = load_item(a, it, next))) {}
                 for (int32_t t = 0; t < w.ntiles; ++t) {
                     const bool more = t + 1 < w.ntiles;
                     const int sv = r.st;   // V(t)
@@ -541,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- the edge of what rows see ----------------
         uint32_t fill = 0, seen = 0;
         bool ok = true;
-        for (int32_t it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
             Item w;
             if (!load_item(a, it, w)) continue;
             for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
@@ -647,19 +720,19 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
 }
 
 template <int D>
-cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int n_ctas, cudaStream_t s) {
+cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, cudaStream_t s) {
     const void* f = (const void*)k_attend_tc<D>;
     cudaError_t e = func_smem_optin(f, Tc<D>::BYTES);
     if (e != cudaSuccess) return e;
-    k_attend_tc<D><<<n_ctas, kThreads, Tc<D>::BYTES, s>>>(a, qmap, kvmap);
+    k_attend_tc<D><<<a.items, kThreads, Tc<D>::BYTES, s>>>(a, qmap, kvmap);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
-                             int n_ctas, cudaStream_t s) {
-    return d == 128 ? launch<128>(a, qmap, kvmap, n_ctas, s) : launch<64>(a, qmap, kvmap, n_ctas, s);
+                             cudaStream_t s) {
+    return d == 128 ? launch<128>(a, qmap, kvmap, s) : launch<64>(a, qmap, kvmap, s);
 }
 
 cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s) {
