@@ -51,10 +51,11 @@ struct Tc {
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
     // barriers: kv_full[STAGES], kv_empty[STAGES], v_ok[STAGES], q_full, q_empty, s_full[2], p_full[2], o_full[2],
-    // drained, next_full[2], next_empty[2]
-    static constexpr int NBAR = 3 * STAGES + 13;
-    static constexpr int OFF_NEXT = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // two answers of the work distributor
-    static constexpr int OFF_MISC = OFF_NEXT + 32;        // tensor memory address, epilogue count, overlay item, error
+    // drained, answer, item_full[2], item_empty[2]
+    static constexpr int NBAR = 3 * STAGES + 14;
+    static constexpr int OFF_ANSWER = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // of the work distributor, 16 bytes
+    static constexpr int OFF_ITEM = OFF_ANSWER + 16;      // two work items
+    static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -166,110 +167,142 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // A work item, the same in every warp
-struct Item {
-    int32_t u, g, rows, r0, first, seen0, lo, split;
-    int32_t nt[2], ntiles;   // key tiles of each row tile, and of the item
-    int32_t lim0;            // last slot that the item's first row sees
-    int32_t end;             // one past the last slot that any row sees in this split
-    bool split_out;
+struct __align__(16) Item {
+    int32_t some;            // 0: there is none left
+    int32_t g, first, rows;  // KV head, first packed row, query rows of the sequence
+    int32_t r0, seen0, lim0; // first row; slots before the first query's own; last slot the first row sees
+    int32_t lo, end;         // keys [lo, end) of this split that any row sees
+    int32_t nt0, nt1, ntiles;   // key tiles of each row tile, and of the item
+    int32_t split;           // of the keys, -1: not split
+    int32_t u, pad[2];
 };
+static_assert(sizeof(Item) == 64, "two items in OFF_ITEM");
+// item number `it` of the grid; false if it has nothing to do
 __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item& w) {
     const View& v = a.v;
     const int32_t i = prefix_find(a.item0, a.nseq, it);
     const int32_t nq = a.nq[i];
+    w.some = 1;
     w.rows = nq << a.gshift;
     const int32_t tiles = (w.rows + kRows - 1) / kRows;
-    const int32_t rem = it - a.item0[i], nsplit = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
-    w.g = rem % v.hkv;
-    const int32_t x = rem / v.hkv;
-    w.split = x % nsplit;
-    w.r0 = (tiles - 1 - x / nsplit) * kRows;
-    w.split_out = nsplit > 1;
-    w.first = a.start[i];
+    const int32_t rem = it - a.item0[i], x = rem / v.hkv;
+    w.g = rem - x * v.hkv;
     w.u = a.u0 + a.brow[i] * v.hkv + w.g;
     const int32_t n = v.len[w.u];
+    const int32_t splits = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
+    const int32_t tile = splits > 1 ? x / splits : x;
+    w.split = splits > 1 ? x - tile * splits : -1;
+    w.r0 = (tiles - 1 - tile) * kRows;
+    w.first = a.start[i];
     if (n < nq || n > v.cap) {
-        if (threadIdx.x == 0) atomicOr(v.err, DEVERR_STATE);
+        if ((threadIdx.x & 31) == 0) atomicOr(v.err, DEVERR_STATE);
         return false;
     }
     w.seen0 = n - nq;
     w.lim0 = w.seen0 + (w.r0 >> a.gshift);
-    w.lo = w.split_out ? w.split * a.chunk : 0;
-    w.end = 0;
-    w.ntiles = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int32_t a0 = w.r0 + 128 * t, a1 = min(a0 + 128, w.rows) - 1;
-        int32_t hi = a0 < w.rows ? w.seen0 + (a1 >> a.gshift) + 1 : 0;
-        if (w.split_out) hi = min(hi, w.lo + a.chunk);
-        w.nt[t] = hi > w.lo ? (hi - w.lo + kKeys - 1) / kKeys : 0;
-        w.end = max(w.end, hi);
-        w.ntiles = max(w.ntiles, w.nt[t]);
-    }
+    w.lo = splits > 1 ? w.split * a.chunk : 0;
+    auto keys_end = [&](int32_t a0) {   // one past the last key that the row tile from row a0 on sees
+        if (a0 >= w.rows) return 0;
+        const int32_t hi = w.seen0 + ((min(a0 + 128, w.rows) - 1) >> a.gshift) + 1;
+        return splits > 1 ? min(hi, w.lo + a.chunk) : hi;
+    };
+    const int32_t e0 = keys_end(w.r0), e1 = keys_end(w.r0 + 128);
+    w.nt0 = max(e0 - w.lo + kKeys - 1, 0) / kKeys;
+    w.nt1 = max(e1 - w.lo + kKeys - 1, 0) / kKeys;
+    w.end = max(e0, e1);
+    w.ntiles = max(w.nt0, w.nt1);
     return w.ntiles > 0;
 }
 // tile t holds slots that the item's first row does not see, or that do not exist
 __device__ __forceinline__ bool edge_tile(const Item& w, int32_t t) { return w.lo + t * kKeys + kKeys - 1 > w.lim0; }
 
-// The work items after the CTA's first.  The grid has a CTA per item; a CTA
-// that has started takes the numbers of CTAs that have not, so the items go
-// out one by one, in order, to whoever is free.  Warp 8 asks for one item
-// ahead (ask()), every role reads the answer (take()); two answers are kept.
-constexpr int kReaders = 12;   // softmax warps, warps 8 and 10, both issuing threads
-struct NextItem {
+// The work items of a CTA.  The grid has a CTA per item; a CTA that has
+// started takes the numbers of CTAs that have not, so the items go out one by
+// one, in order, to whoever is free.  Warp 8 asks for the next number while
+// it loads an item, works out what the item is and hands it to the other
+// roles through shared memory, one item ahead of them.
+constexpr int kReaders = 11;   // softmax warps, both issuing threads, warp 10
+struct Items {
     uint64_t* full;
     uint64_t* empty;
-    uint32_t addr;
+    const Item* slot;
     uint32_t* err;
-    uint32_t k = 1;   // number of the item in question, from the CTA's first on
-    __device__ __forceinline__ int slot() const { return k & 1; }
-    __device__ __forceinline__ uint32_t parity() const { return ((k - 1) >> 1) & 1; }
-    // one thread of warp 8, once an item, until an answer was -1
-    __device__ __forceinline__ bool ask(uint32_t n) {
-        const int s = n & 1;
-        if (n > 2 && !mbar_wait_bounded(&empty[s], ((n - 3) >> 1) & 1, err, kWaitAttend, 0x700)) return false;
-        mbar_arrive_expect_tx(&full[s], 16);
-        asm volatile(
-            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                addr + 16 * s),
-            "r"(smem_u32(&full[s]))
-            : "memory");
-        return true;
-    }
-    __device__ __forceinline__ int32_t read() const {
-        uint32_t ok, x;
-        asm volatile(
-            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-            "ld.shared.b128 h, [%2];\n\t"
-            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-            : "=r"(ok), "=r"(x)
-            : "r"(addr + 16 * slot())
-            : "memory");
-        fence_proxy_async_smem();
-        return ok ? (int32_t)x : -1;
-    }
-    // the next item or -1; a whole warp
-    __device__ __forceinline__ int32_t take(bool& good) {
-        good = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot()], parity(), err, kWaitAttend, 0x701));
-        if (!good) return -1;
-        const int32_t it = read();
+    uint32_t n = 0;   // number of the next item to take
+    // the next item, false if there is none left; a whole warp
+    __device__ __forceinline__ bool take(Item& w) {
+        const uint32_t s = n & 1;
+        if (!warp_wait(&full[s], (n >> 1) & 1, err, 0x700)) return false;
+        w = slot[s];
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot()]);
-        ++k;
-        return it;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
+        ++n;
+        return w.some != 0;
     }
     // the same for one thread
-    __device__ __forceinline__ int32_t take_one(bool& good) {
-        good = good && mbar_wait_bounded(&full[slot()], parity(), err, kWaitAttend, 0x702);
-        if (!good) return -1;
-        const int32_t it = read();
-        mbar_arrive(&empty[slot()]);
-        ++k;
-        return it;
+    __device__ __forceinline__ bool take_one(Item& w) {
+        const uint32_t s = n & 1;
+        if (!mbar_wait_bounded(&full[s], (n >> 1) & 1, err, kWaitAttend, 0x701)) return false;
+        w = slot[s];
+        mbar_arrive(&empty[s]);
+        ++n;
+        return w.some != 0;
     }
 };
+// ask for the number of a CTA that has not started; answered on `bar`
+__device__ __forceinline__ void ask_next(uint32_t answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// the answer: a number, or -1 if every CTA has started
+__device__ __forceinline__ int32_t read_next(uint32_t answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    fence_proxy_async_smem();   // before the next answer is written over it
+    return ok ? (int32_t)x : -1;
+}
+
+// Among each four lanes: x[j] of lane i becomes x[i] of lane j (items of eight words)
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][8], int lane) {
+    const bool hi = lane & 2, lo = lane & 1;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, hi ? x[j][k] : x[j + 2][k], 2);
+            if (hi) x[j][k] = y;
+            else x[j + 2][k] = y;
+        }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, lo ? x[j][k] : x[j + 1][k], 1);
+            if (lo) x[j][k] = y;
+            else x[j + 1][k] = y;
+        }
+}
+// 32 bytes; `wide`: p is 32-byte aligned
+__device__ __forceinline__ void store32(void* p, const uint32_t* x, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -287,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* p_full = s_full + 2;
     uint64_t* o_full = p_full + 2;
     uint64_t* drained = o_full + 2;
-    uint64_t* next_full = drained + 1;
-    uint64_t* next_empty = next_full + 2;
+    uint64_t* answer = drained + 1;
+    uint64_t* item_full = answer + 1;
+    uint64_t* item_empty = item_full + 2;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
     int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
     const View& v = a.v;
@@ -303,19 +337,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_full, 1);
         mbar_init(q_empty, 2);
         mbar_init(drained, 2);
+        mbar_init(answer, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);     // one lane of each softmax warp
             mbar_init(&o_full[i], 1);
-            mbar_init(&next_full[i], 1);
-            mbar_init(&next_empty[i], kReaders);
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], kReaders);
         }
         misc[1] = 0;                      // epilogues done, in warps
-        misc[2] = 0xFFFFFFFFu;            // the item that `over` belongs to
-        misc[3] = *reinterpret_cast<volatile uint32_t*>(v.err) & DEVERR_TIMEOUT;   // a wait gave up: start nothing more
+        misc[2] = 0;                      // the item that `over` belongs to, from 1 on
         fence_mbar_init();
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kvmap);
+    }
+    Item w0;
+    if (warp == 8) {
+        // (a wait gave up in this launch or before: start nothing more)
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(v.err) & DEVERR_TIMEOUT;
+        if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
+        w0.some = !bad;
     }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -327,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    const int32_t it0 = misc[3] ? -1 : (int32_t)blockIdx.x;   // -1: no item (left)
-    NextItem nx{next_full, next_empty, smem_u32(sm + C::OFF_NEXT), v.err};
+    Items items{item_full, item_empty, reinterpret_cast<Item*>(sm + C::OFF_ITEM), v.err};
+    Item w;
 
     if (warp < 8) {
         // ---------------- softmax ----------------
@@ -338,16 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lane_base + 128 * tile, to = tmem + lane_base + 256 + 128 * tile;
         uint32_t sphase = 0, ophase = 0;
         const float c = a.qscale;
+        const bool wide = (((uintptr_t)a.out.p | a.out.ts | a.out.hs) & 31) == 0;
         bool ok = true;
-        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
-            Item w;
-            if (!load_item(a, it, w)) continue;
+        while (ok && items.take(w)) {
             const int32_t row = w.r0 + 128 * tile + 32 * (warp & 3) + lane;
             const int32_t rc = min(row, w.rows - 1);
             const int32_t lim = w.seen0 + (rc >> a.gshift);   // this row sees slots [0, lim]
             const int32_t lim_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3), w.rows - 1) >> a.gshift);
+            const int32_t nt = tile ? w.nt1 : w.nt0;
             float m = -INFINITY, l = 0.f;
-            for (int32_t t = 0; t < w.nt[tile]; ++t) {
+            for (int32_t t = 0; t < nt; ++t) {
                 if (!warp_wait(&s_full[tile], sphase, v.err, 0x100 + t)) { ok = false; break; }
                 sphase ^= 1;
                 tc_fence_after();
@@ -412,25 +453,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&p_full[tile]);
             }
             if (!ok) break;
-            if (w.nt[tile] > 0) {
+            if (nt > 0) {
                 if (!warp_wait(&o_full[tile], ophase, v.err, 0x200)) { ok = false; break; }
                 ophase ^= 1;
                 tc_fence_after();
-                const int32_t tok = w.first + (row >> a.gshift);
-                const int32_t h = (w.g << a.gshift) + (row & ((1 << a.gshift) - 1));
-                const bool over_here = misc[2] == (uint32_t)it;
-                const float inv = w.split_out ? 1.f : 1.0f / l;
-                const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h;
+                const bool over_here = misc[2] == items.n;
+                const float inv = w.split < 0 ? 1.0f / l : 1.f;
+                // lane i of each four ends up with the i-th 32 bytes of four rows' 128
+                const int32_t row4 = row & ~3;
+                uint8_t* dst[4];
 #pragma unroll
-                for (int j = 0; j < D; j += 32) {
-                    uint32_t o[32];
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t tok = w.first + ((row4 + j) >> a.gshift);
+                    const int32_t h = (w.g << a.gshift) + ((row4 + j) & ((1 << a.gshift) - 1));
+                    dst[j] = (w.split < 0 ? a.out.row(tok, h)
+                                          : reinterpret_cast<uint8_t*>(
+                                                a.part + ((int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h) * D)) +
+                             32 * (lane & 3);
+                }
+#pragma unroll
+                for (int j = 0; j < D; j += 64) {
+                    uint32_t o[64];
                     tmem_ld32(o, to + j);
+                    tmem_ld32(o + 32, to + j + 32);
                     tmem_wait_ld();
                     held(o);
+                    held(o + 32);
                     if (over_here) {
                         // non-finite values of the edge tiles, for the rows that see them
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 64; ++i) {
                             float x = __uint_as_float(o[i]);
                             if (over[j + i] <= lim) x += INFINITY;
                             if (over[D + j + i] <= lim) x -= INFINITY;
@@ -438,29 +490,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[i] = __float_as_uint(x);
                         }
                     }
-                    if (row < w.rows) {
-                        if (w.split_out) {
-                            float4* dst = reinterpret_cast<float4*>(a.part + pr * D + j);
+                    uint32_t x[4][8];
+                    if (w.split < 0) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-                        } else {
-                            uint4* dst = reinterpret_cast<uint4*>(a.out.row(tok, h) + 2 * j);
+                        for (int i = 0; i < 32; ++i)
+                            x[i / 8][i % 8] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        quad_transpose(x, lane);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t x[4];
+                        for (int i = 0; i < 4; ++i)
+                            if (row4 + i < w.rows) store32(dst[i] + 2 * j, x[i], wide);
+                    } else {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    x[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                                                       __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                                dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                            }
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i / 8][i % 8] = o[32 * k + i];
+                            quad_transpose(x, lane);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row4 + i < w.rows) store32(dst[i] + 4 * j + 128 * k, x[i], true);
                         }
                     }
                 }
-                if (w.split_out && row < w.rows)
+                if (w.split >= 0 && row < w.rows) {
+                    const int32_t tok = w.first + (row >> a.gshift), h = (w.g << a.gshift) + (row & ((1 << a.gshift) - 1));
+                    const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h;
                     *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
+                }
             }
             __syncwarp();
             if (lane == 0) atomicAdd(const_cast<uint32_t*>(&misc[1]), 1u);
@@ -470,19 +525,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         // ---------------- TMA ----------------
         const int bx = min(v.page_tokens, 128), nb = 128 / bx;   // rows of a box, boxes of a tile
-        uint32_t fill = 0, items = 0, asked = 0;
+        const uint32_t ans = smem_u32(sm + C::OFF_ANSWER);
+        uint32_t fill = 0, n = 0, asked = 0, read = 0;   // n: items handed out
         bool ok = true;
-        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
-            Item w;
-            const bool some = load_item(a, it, w);
-            ok = true;
-            if (lane == 0) ok = nx.ask(nx.k);
+        auto hand_out = [&](const Item& x) {
+            const uint32_t s = n & 1;
+            if (n >= 2) ok = ok && warp_wait(&item_empty[s], ((n - 2) >> 1) & 1, v.err, 0x702);
+            if (!ok) return;
+            if (lane == 0) {
+                *reinterpret_cast<Item*>(sm + C::OFF_ITEM + 64 * s) = x;
+                mbar_arrive(&item_full[s]);
+            }
+            ++n;
+        };
+        auto ask = [&] {
+            if (lane == 0) ask_next(ans, answer);
             ++asked;
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        };
+        // the next item that has something to do; asks on until then
+        auto next_item = [&](Item& x) {
+            x.some = 0;
+            while (ok) {
+                ok = warp_wait(answer, read & 1, v.err, 0x703);
+                if (!ok) return;
+                ++read;
+                const int32_t it = read_next(ans);
+                __syncwarp();
+                if (it < 0 || load_item(a, it, x)) {
+                    x.some = it >= 0;
+                    return;
+                }
+                ask();
+            }
+        };
+        w = w0;
+        if (w.some) {
+            ask();
+            if (w.ntiles == 0) next_item(w);
+        }
+        uint32_t loaded = 0;
+        if (ok) hand_out(w);
+        while (ok && w.some) {
+            if (asked == read) ask();
+            if (loaded > 0) ok = warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x300);
             if (!ok) break;
-            if (!some) continue;
-            if (items > 0 && !warp_wait(q_empty, (items - 1) & 1, v.err, 0x300)) { ok = false; break; }
-            ++items;
+            ++loaded;
             if (lane == 0) {
                 const int tiles = w.r0 + 128 < w.rows ? 2 : 1;
                 mbar_arrive_expect_tx(q_full, tiles * C::TILE);
@@ -491,10 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(sm + C::OFF_Q + t * C::TILE + hf * C::BLOCK, &qmap, 64 * hf, w.g << a.gshift,
                                     w.first + ((w.r0 + 128 * t) >> a.gshift), q_full);
             }
-            for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
+            Item next;
+            const int32_t fills = 2 * w.ntiles, when = min(4, fills);
+            for (int32_t x = 0; ok && x <= fills; ++x) {
+                if (x == when) {
+                    next_item(next);
+                    if (ok) hand_out(next);
+                }
+                if (x == fills || !ok) break;
                 const int st = fill % C::STAGES;
                 const uint32_t use = fill / C::STAGES;
                 if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, v.err, 0x400 + st)) { ok = false; break; }
+                ++fill;
                 const bool is_v = x & 1;
                 const int32_t s0 = w.lo + (x >> 1) * kKeys;
                 // lane -> (box, half); a box wholly past the last visible slot is not loaded
@@ -516,22 +611,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens + (s & (v.page_tokens - 1))),
                                 &kv_full[st]);
             }
+            w = next;
         }
         // every answer and copy has landed and every commit arrived before the CTA ends
-        if (!ok && asked >= nx.k) nx.take(ok), ok = false;
-        if (ok && items > 0) warp_wait(q_empty, (items - 1) & 1, v.err, 0x301);
+        if (asked > read) warp_wait(answer, read & 1, v.err, 0x704);
+        if (loaded > 0) {
+            if (ok) warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x301);
+            else warp_wait(q_full, (loaded - 1) & 1, v.err, 0x302);
+        }
         for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f) {
             const int st = f % C::STAGES;
             const uint32_t par = (f / C::STAGES) & 1;
             if (ok) warp_wait(&kv_empty[st], par, v.err, 0x401);
             else warp_wait(&kv_full[st], par, v.err, 0x402);
         }
-        if (!ok && items > 0) warp_wait(q_full, (items - 1) & 1, v.err, 0x302);
     } else if (warp == 9 || warp == 11) {
         // ---------------- products of row tile 0 (warp 9) and 1 (warp 11) ----------------
         // One thread each.  What it waits for besides P it waits for while
-        // products it has issued are still running, and the next item is read
-        // early: about four products queue, so a late issue is idle time.
+        // products it has issued are still running: about four products
+        // queue, so a late issue is idle time.
         if (elect_one()) {
             constexpr uint32_t id_qk = idesc_of(128, kKeys, false), id_pv = idesc_of(128, D, true);
             const int tile = warp == 9 ? 0 : 1;
@@ -558,12 +656,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i) mma_ts(to, ts + 8 * i, b + i * (2048 >> 4), id_pv, !(first && i == 0));
             };
-            Item w, next;
-            bool have = false;
-            int32_t it = it0;
-            for (; it >= 0 && !(have = load_item(a, it, w)); it = nx.take_one(ok)) {}
+            bool have = items.take_one(w);
             while (have) {
-                const int32_t nt = w.nt[tile];
+                const int32_t nt = tile ? w.nt1 : w.nt0;
                 wait(q_full, qphase, 0x501);
                 qphase ^= 1;
                 wait(&kv_full[r.st], r.ph, 0x500);
@@ -573,8 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&kv_empty[r.st]);
                 if (w.ntiles == 1) mma_commit(q_empty);
                 r.step();
-                have = false;
-                while ((it = nx.take_one(ok)) >= 0 && !(have = load_item(a, it, next))) {}
                 for (int32_t t = 0; t < w.ntiles; ++t) {
                     const bool more = t + 1 < w.ntiles;
                     const int sv = r.st;   // V(t)
@@ -603,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                w = next;
+                have = items.take_one(w);
             }
             // nothing is in flight when the CTA ends, after a wait that gave up neither
             mma_commit(drained);
@@ -614,9 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- the edge of what rows see ----------------
         uint32_t fill = 0, seen = 0;
         bool ok = true;
-        for (int32_t it = it0; it >= 0; it = ok ? nx.take(ok) : -1) {
-            Item w;
-            if (!load_item(a, it, w)) continue;
+        while (ok && items.take(w)) {
             for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
                 const int st = fill % C::STAGES;
                 ok = warp_wait(&kv_full[st], (fill / C::STAGES) & 1, v.err, 0x600);
@@ -638,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
                     if (__any_sync(0xffffffffu, bad)) {
-                        if (misc[2] != (uint32_t)it) {
+                        if (misc[2] != items.n) {
                             // `over` is free once every epilogue before this item has read it
                             const uint64_t t0 = global_ns();
                             while (misc[1] < 8 * seen) {
@@ -665,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         __syncwarp();
                         __threadfence_block();
-                        if (lane == 0) misc[2] = (uint32_t)it;
+                        if (lane == 0) misc[2] = items.n;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
