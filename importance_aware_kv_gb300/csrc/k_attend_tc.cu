@@ -37,8 +37,8 @@ namespace {
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch (384 x 168 of the SM's 64 K); the softmax
 // warps, which hold a row of 128 logits each, take what the others give up:
-// 256 x 208 + 128 x 88 = 384 x 168.
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+// 256 x 216 + 128 x 72 = 384 x 168.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr int kKeys = kTcKeys, kRows = kTcRows;
 
 template <int D>
@@ -50,9 +50,9 @@ struct Tc {
     static constexpr int OFF_Q = 0;                       // two tiles
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
-    // barriers: kv_full[STAGES], kv_empty[STAGES], v_ok[STAGES], q_full, q_empty, s_full[2], p_full[2], o_full[2],
+    // barriers: kv_full[STAGES], kv_empty[STAGES], v_ok[STAGES], q_full, q_empty, s_full[2], p_full[2][2], o_full[2],
     // drained, answer, item_full[2], item_empty[2]
-    static constexpr int NBAR = 3 * STAGES + 14;
+    static constexpr int NBAR = 3 * STAGES + 16;
     static constexpr int OFF_ANSWER = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // of the work distributor, 16 bytes
     static constexpr int OFF_ITEM = OFF_ANSWER + 16;      // two work items
     static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_empty = q_full + 1;
     uint64_t* s_full = q_empty + 1;
     uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;
+    uint64_t* o_full = p_full + 4;   // p_full: [tile][half of the keys]
     uint64_t* drained = o_full + 2;
     uint64_t* answer = drained + 1;
     uint64_t* item_full = answer + 1;
@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(answer, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);     // one lane of each softmax warp
+            mbar_init(&p_full[2 * i], 4);   // one lane of each softmax warp
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], kReaders);
@@ -445,12 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p[j] = pack_bf16x2(e.x, e.y);
                     }
                     tmem_st16(ts + 16 * k, p);
+                    if (k & 1) {   // half of the keys: their product with V may start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * tile + k / 2]);
+                    }
                 }
                 l += sum.x + sum.y;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[tile]);
             }
             if (!ok) break;
             if (nt > 0) {
@@ -651,10 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit(&s_full[tile]);
             };
-            auto pv = [&](int st, bool first) {   // O += P V
+            auto pv = [&](int st, int half, bool first) {   // O += P V of half of the tile's keys
                 const uint64_t b = dv + st * (C::TILE >> 4);
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i) mma_ts(to, ts + 8 * i, b + i * (2048 >> 4), id_pv, !(first && i == 0));
+                for (int j = 0; j < kKeys / 32; ++j) {
+                    const int i = half * (kKeys / 32) + j;
+                    mma_ts(to, ts + 8 * i, b + i * (2048 >> 4), id_pv, !(first && i == 0));
+                }
             };
             bool have = items.take_one(w);
             while (have) {
@@ -679,11 +685,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.step();
                     if (more) wait(&kv_full[r.st], r.ph, 0x506);   // K(t + 1)
                     if (t < nt) {
-                        wait(&p_full[tile], pphase, 0x503);
+                        wait(&p_full[2 * tile], pphase, 0x503);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(sv, 0, t == 0);
+                        wait(&p_full[2 * tile + 1], pphase, 0x507);
                         pphase ^= 1;
                         if (!ok) break;
                         tc_fence_after();
-                        pv(sv, t == 0);
+                        pv(sv, 1, false);
                         if (t + 1 < nt) qk(r.st);
                         else mma_commit(&o_full[tile]);
                     }
