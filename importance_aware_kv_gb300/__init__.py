@@ -9,6 +9,7 @@ or PyTorch fallback, and importing this package fails loudly when
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -189,6 +190,7 @@ class Rope:
         if cos.device != sin.device:
             raise ValueError("cos and sin are on different devices")
         self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self.device_index = cos.device.index
         self.c = hikv_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
 
 
@@ -344,6 +346,7 @@ class Cache:
         self.h = hikv_create_cache(cfg)
         import torch
         self.device_index = torch.cuda.current_device()
+        self._torch_dtype = self._dtype()
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
@@ -383,27 +386,42 @@ class Cache:
         hikv_append(self.h, layer0, k, v, stream)
 
     def _counts(self, counts, name):
-        """HOST int32 [batch] from a list, array or CPU tensor of whole numbers."""
-        a = np.asarray(counts)
-        if a.dtype.kind not in "iu":
-            raise TypeError(f"{name} must hold whole numbers")
-        if a.shape != (self.cfg.batch,):
-            raise ValueError(f"{name} has shape {a.shape}, expected ({self.cfg.batch},)")
-        if a.size and (a.min() < -1 or a.max() > 0x7FFFFFFF):
+        """HOST int32 [batch] (its address, its sum, what keeps it alive) from
+        a list, array or CPU tensor of whole numbers."""
+        batch = self.cfg.batch
+        if type(counts) in (list, tuple) and len(counts) == batch and set(map(type, counts)) == {int}:
+            try:
+                a = array.array("i", counts)
+            except OverflowError:
+                raise ValueError(f"{name} holds values out of range") from None
+            low, total, ptr = min(a), sum(a), a.buffer_info()[0]
+        else:
+            a = np.asarray(counts)
+            if a.dtype.kind not in "iu":
+                raise TypeError(f"{name} must hold whole numbers")
+            if a.shape != (batch,):
+                raise ValueError(f"{name} has shape {a.shape}, expected ({batch},)")
+            if a.max() > 0x7FFFFFFF or a.min() < -1:
+                raise ValueError(f"{name} holds values out of range")
+            a = np.ascontiguousarray(a, dtype=np.int32)
+            low, total, ptr = int(a.min()), int(a.sum(dtype=np.int64)), a.ctypes.data
+        if low < -1:
             raise ValueError(f"{name} holds values out of range")
-        return np.ascontiguousarray(a, dtype=np.int32)
+        return ptr, total, a
 
     def _rows(self, t, name, total, heads):
         """Packed rows [tokens][heads][head_dim] as the C ABI's hikv_rows."""
         import torch
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.device.index != self.device_index:
+        if t.get_device() != self.device_index:
             raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device_index}")
-        self._check_tensor(t, name, (total, heads, self.cfg.head_dim))
-        if t.stride(2) != 1:
+        if t.dtype is not self._torch_dtype or t.shape != (total, heads, self.cfg.head_dim):
+            self._check_tensor(t, name, (total, heads, self.cfg.head_dim))
+        stride = t.stride()
+        if stride[2] != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        return hikv_rows(t.data_ptr(), t.stride(0), t.stride(1))
+        return hikv_rows(t.data_ptr(), stride[0], stride[1])
 
     def append_packed(self, k, v, ntok, layer=0, q=None, q_out=None, rope=None, stream=None):
         """Append a packed batch to one layer: k, v [sum ntok][Hkv][d] (any
@@ -412,40 +430,49 @@ class Cache:
         enters the cache, and q [sum ntok][Hq][d], if given, into q_out (may
         be q itself)."""
         c = self.cfg
-        n = self._counts(ntok, "ntok")
-        total = int(n.sum(dtype=np.int64))
-        rows = [self._rows(k, "k", total, c.num_kv_heads), self._rows(v, "v", total, c.num_kv_heads)]
+        n, total, _keep = self._counts(ntok, "ntok")
+        rk, rv = self._rows(k, "k", total, c.num_kv_heads), self._rows(v, "v", total, c.num_kv_heads)
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
-        rows += [self._rows(t, name, total, c.num_q_heads) if t is not None else None
-                 for t, name in ((q, "q"), (q_out, "q_out"))]
-        if rope is not None and rope.cos.device.index != self.device_index:
-            raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
-        _check(_lib.hikv_append_packed(self.h, layer, n.ctypes.data, *[ctypes.byref(r) if r else None for r in rows],
-                                       ctypes.byref(rope.c) if rope is not None else None,
-                                       _stream_of(k, stream)))
+        rq = ro = rc = None
+        if q is not None:
+            rq = ctypes.byref(self._rows(q, "q", total, c.num_q_heads))
+            ro = ctypes.byref(self._rows(q_out, "q_out", total, c.num_q_heads))
+        if rope is not None:
+            if rope.device_index != self.device_index:
+                raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
+            rc = ctypes.byref(rope.c)
+        _check(_lib.hikv_append_packed(self.h, layer, n, ctypes.byref(rk), ctypes.byref(rv), rq, ro, rc,
+                                       self._stream_int(stream)))
 
     def attend_packed(self, q, out, nq, layer=0, stream=None):
         """Causal attention of the newest nq[b] positions of every sequence
         over everything its units hold up to them: q, out [sum nq][Hq][d]
         (any 16-byte strides).  Append the positions' tokens first."""
         c = self.cfg
-        n = self._counts(nq, "nq")
-        total = int(n.sum(dtype=np.int64))
+        n, total, _keep = self._counts(nq, "nq")
         rq, ro = self._rows(q, "q", total, c.num_q_heads), self._rows(out, "out", total, c.num_q_heads)
-        _check(_lib.hikv_attend_packed(self.h, layer, n.ctypes.data, ctypes.byref(rq), ctypes.byref(ro),
-                                       _stream_of(q, stream)))
+        _check(_lib.hikv_attend_packed(self.h, layer, n, ctypes.byref(rq), ctypes.byref(ro),
+                                       self._stream_int(stream)))
 
     def drop(self, counts=None, layer0=0, nlayers=None, stream=None):
         """Drop the newest counts[b] tokens of every unit of batch row b (-1,
         or counts None: all); their positions are free again."""
-        n = None if counts is None else self._counts(counts, "counts")
+        n, _, _keep = (None, 0, None) if counts is None else self._counts(counts, "counts")
         nl = self.cfg.num_layers - layer0 if nlayers is None else nlayers
-        _check(_lib.hikv_drop(self.h, layer0, nl, None if n is None else n.ctypes.data, self._own_stream(stream)))
+        _check(_lib.hikv_drop(self.h, layer0, nl, n, self._stream_int(stream)))
 
-    def _own_stream(self, stream):
+    def _stream_int(self, stream):
+        """The given stream, else the current one of the cache's device."""
+        if stream is not None:
+            return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        global _RAW_STREAM
+        if _RAW_STREAM is None:
+            _RAW_STREAM = _raw_stream_fn() or False
+        if _RAW_STREAM:
+            return _RAW_STREAM(self.device_index)
         import torch
-        return _stream(torch.cuda.current_stream(self.device_index) if stream is None else stream)
+        return torch.cuda.current_stream(self.device_index).cuda_stream
 
     def device_view(self) -> dict:
         """The cache's own device memory as tensors, without a copy: pages

@@ -172,6 +172,17 @@ __device__ __forceinline__ uint8_t* row_ptr(const View& v, int32_t u, int32_t s,
            ((is_v ? (int64_t)v.page_tokens : 0) + r) * v.row_bytes;
 }
 
+// The same through unit_page (no table read with home pages).
+__device__ __forceinline__ uint8_t* slot_row(const View& v, int32_t u, int32_t s, bool is_v) {
+    const int32_t pg = unit_page(v, u, s);
+    if (pg < 0 || pg >= v.pool_pages) {
+        atomicOr(v.err, DEVERR_PAGE);
+        return nullptr;
+    }
+    const int32_t r = s & (v.page_tokens - 1);
+    return v.pool + (int64_t)pg * v.page_bytes + ((is_v ? (int64_t)v.page_tokens : 0) + r) * v.row_bytes;
+}
+
 // Per unit: reserve ntok slots and map the pages they need.  Writes the
 // first slot to base[u - u0] (-1 when the pool ran dry, which the host's
 // capacity check makes impossible).
@@ -612,9 +623,12 @@ struct PackedAppendArgs {
     const float* cos;       // null: no rotation
     const float* sin;
     int32_t rot, interleaved;
-    int32_t* base;          // scratch [units]: first slot of this append
+    int32_t slices;         // warps a token (set by the launch)
+    int32_t pos0[kSeqMax];  // position of each sequence's first token
+    int32_t base[kSeqMax];  // its slot, where the sequence's heads all hold as many tokens, else ...
+    int32_t* reserved;      // ... scratch [units]: reserve slots and pages in a launch of their own (null: base)
 };
-cudaError_t launch_append_packed(const PackedAppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_append_packed(PackedAppendArgs& a, int dtype, int sm_count, cudaStream_t s);
 
 // Causal attention of packed queries over the cache (hikv_attend_packed).
 // Query row r of a (sequence, KV head) is token r / G, head r % G of its

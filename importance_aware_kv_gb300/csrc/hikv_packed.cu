@@ -166,7 +166,6 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         a.rot = rope->rot_dim;
         a.interleaved = rope->interleaved;
     }
-    a.base = c->d_append_base;
     int32_t row = 0;
     for (int b0 = 0; b0 < c->B; b0 += kSeqMax) {
         const int n = std::min(kSeqMax, c->B - b0);
@@ -178,8 +177,19 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         }
         a.seqs.start[n] = row;
         if (row == a.seqs.start[0]) continue;
-        cudaError_t e = launch_append_packed(a, c->dtype, (cudaStream_t)stream);
-        c->launches += 2;
+        // one launch where the host knows every slot: equal heads, no page to take
+        bool known = true;
+        for (int i = 0; i < n; ++i) {
+            const int ub = u0 + (b0 + i) * c->Hkv;
+            a.pos0[i] = c->next_pos[ub];
+            a.base[i] = c->len[ub];
+            if (ntok[b0 + i] == 0) continue;
+            for (int u = ub; u < ub + c->Hkv; ++u)
+                known &= c->len[u] == c->len[ub] && ceil_div(c->len[u] + ntok[b0 + i], c->P) <= c->mapped[u];
+        }
+        a.reserved = known ? nullptr : c->d_append_base;
+        cudaError_t e = launch_append_packed(a, c->dtype, c->sm_count, (cudaStream_t)stream);
+        c->launches += known ? 1 : 2;
         if (e != cudaSuccess) return cuda_fail(e, "append_packed: launch");
         for (int i = 0; i < n * c->Hkv; ++i) {
             const int u = u0 + b0 * c->Hkv + i, m = ntok[b0 + i / c->Hkv];

@@ -20,7 +20,7 @@ def cache(hk):
     c = hk.Cache.__new__(hk.Cache)
     c.cfg = hk.CacheConfig(num_layers=1, batch=2, num_q_heads=4, num_kv_heads=2, head_dim=64, dtype="bf16",
                            num_sink=0, recent_window=0, budgets=[8, 8], max_tokens=16)
-    c.h, c.device_index = None, 0
+    c.h, c.device_index, c._torch_dtype = None, 0, torch.bfloat16
     return c
 
 
