@@ -126,20 +126,22 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
             return fail(HIKV_ERR_UNSUPPORTED, "append_packed: rot_dim %d is no multiple of 16 up to head_dim %d",
                         rope->rot_dim, c->d);
     }
-    const int u0 = layer * c->per_layer;
+    const int u0 = layer * c->per_layer, Hkv = c->Hkv;
     int64_t new_pages = 0;
     for (int b = 0; b < c->B; ++b) {
-        if (ntok[b] == 0) continue;
-        const int ub = u0 + b * c->Hkv;
-        for (int u = ub; u < ub + c->Hkv; ++u) {
-            if ((int64_t)c->len[u] + ntok[b] > c->cap)
-                return fail(HIKV_ERR_CAPACITY, "append_packed: unit %d would hold %lld > max_tokens %d", u,
-                            (long long)c->len[u] + ntok[b], c->cap);
-            if (c->next_pos[u] != c->next_pos[ub])
-                return fail(HIKV_ERR_STATE, "append_packed: units %d and %d are at different positions", u, ub);
-            new_pages += std::max(0, ceil_div(c->len[u] + ntok[b], c->P) - c->mapped[u]);
+        const int m = ntok[b];
+        if (m == 0) continue;
+        const int ub = u0 + b * Hkv;
+        const int32_t *len = c->len.data() + ub, *mapped = c->mapped.data() + ub, *next_pos = c->next_pos.data() + ub;
+        for (int g = 0; g < Hkv; ++g) {
+            if ((int64_t)len[g] + m > c->cap)
+                return fail(HIKV_ERR_CAPACITY, "append_packed: unit %d would hold %lld > max_tokens %d", ub + g,
+                            (long long)len[g] + m, c->cap);
+            if (next_pos[g] != next_pos[0])
+                return fail(HIKV_ERR_STATE, "append_packed: units %d and %d are at different positions", ub + g, ub);
+            new_pages += std::max(0, ((len[g] + m - 1) >> c->page_shift) + 1 - mapped[g]);
         }
-        const int64_t end = (int64_t)c->next_pos[ub] + ntok[b];
+        const int64_t end = (int64_t)next_pos[0] + m;
         if (end > INT32_MAX) return fail(HIKV_ERR_CAPACITY, "append_packed: positions of batch row %d overflow int32", b);
         if (rope && end > rope->positions)
             return fail(HIKV_ERR_INVALID_ARG, "append_packed: batch row %d reaches position %lld, the rope has %d", b,
@@ -180,27 +182,31 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         // one launch where the host knows every slot: equal heads, no page to take
         bool known = true;
         for (int i = 0; i < n; ++i) {
-            const int ub = u0 + (b0 + i) * c->Hkv;
+            const int ub = u0 + (b0 + i) * Hkv, m = ntok[b0 + i];
+            const int32_t *len = c->len.data() + ub, *mapped = c->mapped.data() + ub;
             a.pos0[i] = c->next_pos[ub];
-            a.base[i] = c->len[ub];
-            if (ntok[b0 + i] == 0) continue;
-            for (int u = ub; u < ub + c->Hkv; ++u)
-                known &= c->len[u] == c->len[ub] && ceil_div(c->len[u] + ntok[b0 + i], c->P) <= c->mapped[u];
+            a.base[i] = len[0];
+            if (m == 0) continue;
+            for (int g = 0; g < Hkv; ++g) known &= len[g] == len[0] && ((len[g] + m - 1) >> c->page_shift) < mapped[g];
         }
         a.reserved = known ? nullptr : c->d_append_base;
         cudaError_t e = launch_append_packed(a, c->dtype, c->sm_count, (cudaStream_t)stream);
         c->launches += known ? 1 : 2;
         if (e != cudaSuccess) return cuda_fail(e, "append_packed: launch");
-        for (int i = 0; i < n * c->Hkv; ++i) {
-            const int u = u0 + b0 * c->Hkv + i, m = ntok[b0 + i / c->Hkv];
+        for (int i = 0; i < n; ++i) {
+            const int m = ntok[b0 + i], ub = u0 + (b0 + i) * Hkv;
             if (m == 0) continue;
-            c->len[u] += m;
-            c->next_pos[u] += m;
-            c->tail[u] += m;
-            const int mapped = std::max(c->mapped[u], ceil_div(c->len[u], c->P));
-            c->pages_in_use += mapped - c->mapped[u];
-            c->mapped[u] = mapped;
-            c->fresh[u] = 0;
+            for (int u = ub; u < ub + Hkv; ++u) {
+                c->len[u] += m;
+                c->next_pos[u] += m;
+                c->tail[u] += m;
+                c->fresh[u] = 0;
+                const int pages = ((c->len[u] - 1) >> c->page_shift) + 1;
+                if (pages > c->mapped[u]) {
+                    c->pages_in_use += pages - c->mapped[u];
+                    c->mapped[u] = pages;
+                }
+            }
         }
     }
     return HIKV_OK;
@@ -299,7 +305,7 @@ hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* 
     set_last_error("");
     NvtxRange nvtx("hikv_drop");
     if (!range_ok(c, layer0, nl)) return fail(HIKV_ERR_INVALID_ARG, "drop: bad cache or layer range");
-    const int u0 = layer0 * c->per_layer, nu = nl * c->per_layer;
+    const int u0 = layer0 * c->per_layer;
     auto count = [&](int b) { return ndrop ? ndrop[b] : -1; };
     bool any = false;
     for (int b = 0; b < c->B; ++b) {
@@ -307,10 +313,13 @@ hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* 
         any |= count(b) != 0;
     }
     if (!any) return HIKV_OK;
-    for (int u = u0; u < u0 + nu; ++u) {
-        const int n = count(u % c->per_layer / c->Hkv);
-        if (n > c->tail[u])
-            return fail(HIKV_ERR_STATE, "drop: %d tokens of unit %d, which holds its newest %d in order", n, u, c->tail[u]);
+    const int rows = nl * c->B;   // (layer, batch row) pairs
+    for (int r = 0; r < rows; ++r) {
+        const int n = count(r % c->B), ub = u0 + r * c->Hkv;
+        for (int u = ub; u < ub + c->Hkv; ++u)
+            if (n > c->tail[u])
+                return fail(HIKV_ERR_STATE, "drop: %d tokens of unit %d, which holds its newest %d in order", n, u,
+                            c->tail[u]);
     }
     DeviceGuard guard(c->device);
     if (guard.status != cudaSuccess) return cuda_fail(guard.status, "drop: device");
@@ -327,17 +336,20 @@ hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* 
         c->launches += 1;
         if (e != cudaSuccess) return cuda_fail(e, "drop: launch");
     }
-    for (int u = u0; u < u0 + nu; ++u) {
-        const int n = count(u % c->per_layer / c->Hkv);
+    for (int r = 0; r < rows; ++r) {
+        const int n = count(r % c->B), ub = u0 + r * c->Hkv;
         if (n == 0) continue;
-        c->len[u] = n < 0 ? 0 : c->len[u] - n;
-        c->next_pos[u] = n < 0 ? 0 : c->next_pos[u] - n;
-        c->tail[u] = n < 0 ? 0 : c->tail[u] - n;
-        c->fresh[u] = 0;
-        if (!c->v.home_pages) {
-            const int mapped = std::min(c->mapped[u], ceil_div(c->len[u], c->P));
-            c->pages_in_use -= c->mapped[u] - mapped;
-            c->mapped[u] = mapped;
+        for (int u = ub; u < ub + c->Hkv; ++u) {
+            const int left = n < 0 ? 0 : c->len[u] - n;
+            c->next_pos[u] = n < 0 ? 0 : c->next_pos[u] - n;
+            c->tail[u] = n < 0 ? 0 : c->tail[u] - n;
+            c->len[u] = left;
+            c->fresh[u] = 0;
+            if (!c->v.home_pages) {
+                const int mapped = std::min(c->mapped[u], ceil_div(left, c->P));
+                c->pages_in_use -= c->mapped[u] - mapped;
+                c->mapped[u] = mapped;
+            }
         }
     }
     return HIKV_OK;
