@@ -36,7 +36,8 @@ __global__ void k_reserve_packed(const __grid_constant__ PackedAppendArgs a) {
 }
 
 constexpr int kWarps = 8;
-constexpr int kBatch = 4;   // rows a lane has in flight
+constexpr int kBatch = 2;   // rows a lane has in flight; with 32 warps an SM (64 registers) 208 us for 4 x 8192
+                            // tokens of 64/8 heads, four rows and 16 warps 225 us, four and 32 warps 236 us
 
 template <typename T, int VE>
 __device__ __forceinline__ void unpack(const uint4& x, float* f);
@@ -78,7 +79,7 @@ __device__ __forceinline__ void turn(uint4& cx, uint4& cy, const float* c, const
 }
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) k_append_packed(const __grid_constant__ PackedAppendArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) k_append_packed(const __grid_constant__ PackedAppendArgs a) {
     constexpr int VE = 16 / (int)sizeof(T);      // elements of a chunk
     constexpr int PAIRS = D / (2 * VE);          // chunk pairs of a row
     constexpr int ROWS = 32 / PAIRS;             // rows a warp covers at once
