@@ -490,6 +490,25 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Launch `kernel` so that it may start before the previous grid in the stream
+// has ended (programmatic dependent launch): every thread must call
+// griddep_wait() before it touches anything another kernel reads or writes.
+template <typename... P, typename... A>
+inline cudaError_t launch_overlapped(void (*kernel)(P...), int32_t grid, int32_t threads, size_t smem, cudaStream_t s,
+                                     const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // shared::cluster address of `p` in CTA `rank` of this cluster
 __device__ __forceinline__ uint32_t dsmem_addr(const void* p, uint32_t rank) {
     uint32_t r;

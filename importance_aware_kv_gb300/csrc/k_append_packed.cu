@@ -25,6 +25,8 @@ namespace {
 // thread per (sequence, KV head): reserve the slots and map their pages
 __global__ void k_reserve_packed(const __grid_constant__ PackedAppendArgs a) {
     const int32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();
     if (i >= a.seqs.n * a.v.hkv) return;
     const int32_t b = i / a.v.hkv;
     const int32_t ntok = a.seqs.start[b + 1] - a.seqs.start[b];
@@ -88,6 +90,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_append_packed(const __grid_c
     const int32_t gw = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int32_t tok = gw / a.slices, slice = gw - tok * a.slices;
     const int32_t t = a.seqs.start[0] + tok;
+    griddep_launch_dependents();
+    griddep_wait();   // the rows' producer, and whoever still reads the pages
     if (t >= a.seqs.start[a.seqs.n]) return;
     const int32_t b = prefix_find(a.seqs.start, a.seqs.n, t);
     const int32_t u0 = a.u0 + (a.seqs.row0 + b) * v.hkv;
@@ -163,6 +167,8 @@ __global__ void __launch_bounds__(128) k_drop(const __grid_constant__ DropArgs a
     const View& v = a.v;
     const int32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     const int32_t per_layer = a.n * v.hkv;
+    griddep_launch_dependents();
+    griddep_wait();
     if (w >= a.nlayers * per_layer) return;
     const int32_t b = w % per_layer / v.hkv;
     const int32_t u = ((a.layer0 + w / per_layer) * v.batch + a.row0 + b) * v.hkv + w % v.hkv;
@@ -199,37 +205,30 @@ __global__ void __launch_bounds__(128) k_drop(const __grid_constant__ DropArgs a
 
 namespace {
 template <typename T, int D>
-void launch_rows(const PackedAppendArgs& a, int32_t grid, cudaStream_t s) {
-    if (a.interleaved) k_append_packed<T, D, true><<<grid, 32 * kWarps, 0, s>>>(a);
-    else k_append_packed<T, D, false><<<grid, 32 * kWarps, 0, s>>>(a);
+cudaError_t launch_rows(const PackedAppendArgs& a, int32_t grid, cudaStream_t s) {
+    return a.interleaved ? launch_overlapped(k_append_packed<T, D, true>, grid, 32 * kWarps, 0, s, a)
+                         : launch_overlapped(k_append_packed<T, D, false>, grid, 32 * kWarps, 0, s, a);
 }
 }  // namespace
 
 cudaError_t launch_append_packed(PackedAppendArgs& a, int dtype, int sm_count, cudaStream_t s) {
     const int32_t total = a.seqs.start[a.seqs.n] - a.seqs.start[0];
     if (a.reserved) {
-        k_reserve_packed<<<ceil_div(a.seqs.n * a.v.hkv, 128), 128, 0, s>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_overlapped(k_reserve_packed, ceil_div(a.seqs.n * a.v.hkv, 128), 128, 0, s, a);
         if (e != cudaSuccess) return e;
     }
     // warps a token: enough to give every SM sixteen, at most one per warpful of rows
     const int rows = (a.q.p ? a.v.hq : 0) + 2 * a.v.hkv, at_once = 32 * 32 / a.v.row_bytes;
     a.slices = std::max(1, std::min(ceil_div(rows, at_once), ceil_div(16 * sm_count, total)));
     const int32_t grid = (int32_t)(((int64_t)total * a.slices + kWarps - 1) / kWarps);
-    if (dtype == HIKV_BF16) {
-        if (a.v.d == 128) launch_rows<__nv_bfloat16, 128>(a, grid, s);
-        else launch_rows<__nv_bfloat16, 64>(a, grid, s);
-    } else {
-        if (a.v.d == 128) launch_rows<float, 128>(a, grid, s);
-        else launch_rows<float, 64>(a, grid, s);
-    }
-    return cudaGetLastError();
+    if (dtype == HIKV_BF16)
+        return a.v.d == 128 ? launch_rows<__nv_bfloat16, 128>(a, grid, s) : launch_rows<__nv_bfloat16, 64>(a, grid, s);
+    return a.v.d == 128 ? launch_rows<float, 128>(a, grid, s) : launch_rows<float, 64>(a, grid, s);
 }
 
 cudaError_t launch_drop(const DropArgs& a, cudaStream_t s) {
     const int32_t warps = a.nlayers * a.n * a.v.hkv;
-    k_drop<<<ceil_div(warps, 4), 128, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(k_drop, ceil_div(warps, 4), 128, 0, s, a);
 }
 
 }  // namespace hikv

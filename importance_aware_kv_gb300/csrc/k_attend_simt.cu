@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
     float* Ps = sm + C::OFF_P;
     const View& v = a.v;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    griddep_launch_dependents();
+    griddep_wait();
     const int32_t i0 = prefix_find(a.item0, a.nseq, blockIdx.x);
     const int32_t nq = a.nq[i0], first = a.start[i0];
     const int32_t g = (blockIdx.x - a.item0[i0]) % v.hkv;
@@ -179,8 +181,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
     const size_t smem = Simt<D>::FLOATS * sizeof(float);
     cudaError_t e = func_smem_optin(f, smem);
     if (e != cudaSuccess) return e;
-    k_attend_simt<D><<<a.items, kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(k_attend_simt<D>, a.items, kThreads, smem, s, a);
 }
 
 }  // namespace

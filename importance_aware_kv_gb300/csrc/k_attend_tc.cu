@@ -355,18 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kvmap);
     }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(sm + C::OFF_MISC))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    griddep_wait();   // what the kernel before writes is there: lengths, pages, q
     Item w0;
     if (warp == 8) {
         // (a wait gave up in this launch or before: start nothing more)
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(v.err) & DEVERR_TIMEOUT;
         if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
         w0.some = !bad;
-    }
-    if (warp == 9) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         smem_u32(sm + C::OFF_MISC))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -796,6 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a) {
     const View& v = a.v;
+    griddep_launch_dependents();
+    griddep_wait();
     const int32_t x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t tok = x / v.hq, h = x % v.hq;
     if (tok >= a.comb0[a.nseq]) return;
@@ -828,8 +831,7 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
     const void* f = (const void*)k_attend_tc<D>;
     cudaError_t e = func_smem_optin(f, Tc<D>::BYTES);
     if (e != cudaSuccess) return e;
-    k_attend_tc<D><<<a.items, kThreads, Tc<D>::BYTES, s>>>(a, qmap, kvmap);
-    return cudaGetLastError();
+    return launch_overlapped(k_attend_tc<D>, a.items, kThreads, Tc<D>::BYTES, s, a, qmap, kvmap);
 }
 
 }  // namespace
@@ -841,9 +843,8 @@ cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const
 
 cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s) {
     const int32_t grid = (int32_t)(((int64_t)a.comb0[a.nseq] * a.v.hq + 3) / 4);
-    if (d == 128) k_attend_join<128><<<grid, 128, 0, s>>>(a);
-    else k_attend_join<64><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+    return d == 128 ? launch_overlapped(k_attend_join<128>, grid, 128, 0, s, a)
+                    : launch_overlapped(k_attend_join<64>, grid, 128, 0, s, a);
 }
 
 }  // namespace hikv
