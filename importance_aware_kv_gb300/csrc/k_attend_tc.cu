@@ -118,6 +118,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t addr) {
 __device__ __forceinline__ void held(uint32_t* r) {
     asm volatile("" : RW8(r, 0), RW8(r, 8), RW8(r, 16), RW8(r, 24));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t* r, uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : R8(r, 0) : "r"(addr));
+}
+__device__ __forceinline__ void held8(uint32_t* r) { asm volatile("" : RW8(r, 0)); }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::I8(r, 0), "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -422,14 +430,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = m == mt ? 1.f : ex2((m - mt) * c);
                     if (t > 0) {
 #pragma unroll
-                        for (int j = 0; j < D; j += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(o, to + j);
+                        for (int j = 0; j < D; j += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(o, to + j);
                             tmem_wait_ld();
-                            held(o);
+                            held8(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32(to + j, o);
+                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st8(to + j, o);
                         }
                     }
                     l *= f;
