@@ -58,7 +58,7 @@ struct Tc {
     static constexpr int NBAR = 3 * STAGES + 16;
     static constexpr int OFF_ANSWER = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // of the work distributor, 16 bytes
     static constexpr int OFF_ITEM = OFF_ANSWER + 16;      // two work items
-    static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item
+    static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item, turn
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -176,6 +176,19 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
+
+// a turn between the two issuing threads (it orders no memory)
+__device__ __forceinline__ bool turn_begin(uint32_t* turn, uint32_t* err) {
+    if (atomicExch(turn, 1u) == 0u) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0; i < (1u << 28); ++i) {
+        if (atomicExch(turn, 1u) == 0u) return true;
+        if ((i & 255u) == 255u && global_ns() - t0 > kWaitLimitNs) break;
+    }
+    record_timeout(err, kWaitAttend, 0x508, global_ns() - t0);
+    return false;
+}
+__device__ __forceinline__ void turn_end(uint32_t* turn) { atomicExch(turn, 0u); }
 
 // A work item, the same in every warp
 struct __align__(16) Item {
@@ -358,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&item_empty[i], kReaders);
         }
         misc[1] = 0;                      // epilogues done, in warps
+        misc[3] = 0;                      // a row tile is issuing the products between two of its softmaxes
         misc[2] = 0;                      // the item that `over` belongs to, from 1 on
         fence_mbar_init();
         prefetch_tensormap(&qmap);
@@ -703,11 +717,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pv(sv, 0, t == 0);
                         wait(&p_full[2 * tile + 1], pphase, 0x507);
                         pphase ^= 1;
+                        // One row tile at a time from here to its next S: sharing the
+                        // tensor cores, two tiles in step would stay in step, their
+                        // softmaxes at once and then their products at once.
+                        ok = ok && turn_begin(const_cast<uint32_t*>(&misc[3]), v.err);
                         if (!ok) break;
                         tc_fence_after();
                         pv(sv, 1, false);
                         if (t + 1 < nt) qk(r.st);
                         else mma_commit(&o_full[tile]);
+                        turn_end(const_cast<uint32_t*>(&misc[3]));
                     }
                     if (!ok) break;
                     mma_commit(&kv_empty[sv]);
