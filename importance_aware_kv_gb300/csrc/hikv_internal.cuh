@@ -663,7 +663,7 @@ struct AttendArgs {
     int32_t gshift;         // log2(G)
     RowsArg q, out;
     float qscale;           // scale * log2(e)
-    int32_t chunk;          // keys per split (a multiple of 128)
+    int32_t chunk;          // keys per split (a multiple of the kernel's key tile)
     float* part;            // partial results of split items: [splits][part_rows][d] outputs, ...
     float* part_ml;         // ... [splits][part_rows][2] maxima and sums
     int64_t part_rows;      // rows (t, h) of the packed batch
@@ -686,11 +686,12 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
 }
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s);
 constexpr int kSimtRows = 64;   // query rows of a work item of that kernel
+constexpr int kSimtKeys = 64;   // keys per tile
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
                              cudaStream_t s);
 constexpr int kTcRows = 256;    // of the tensor-core kernel
 constexpr int kTcKeys = 128;    // keys per tile
-cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s);
+cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s);
 
 constexpr int kDropMax = 512;
 struct DropArgs {

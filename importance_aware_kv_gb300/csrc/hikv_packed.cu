@@ -45,46 +45,54 @@ int64_t packed_total(const hikv_cache* c, const int32_t* ntok) {
     return total <= INT32_MAX ? total : -1;
 }
 
-// Keys per split of a tensor-core launch, a multiple of the key tile
-// (INT32_MAX: no split).  A CTA works through its items at about one key tile
-// a step and spends about kItemSteps more on each (its first loads, its
-// epilogue); the splits' partial results cost a second launch and their
-// traffic.  The candidates cut the longest sequence into 1 .. 64 parts.
+// The shape of the work items of the tensor-core and of the CUDA-core kernel:
+// query rows, keys per step, CTAs an SM runs at once, and what an item and
+// the join of split results cost beside the steps, in steps (fitted: about
+// 1.5 us a step of the first kernel, 3 of the second).
+struct ItemShape {
+    int rows, keys, resident;
+    double item_steps, join_steps;
+};
+constexpr ItemShape kTcShape{kTcRows, kTcKeys, 1, 3.0, 4.0};
+constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 1.0, 2.0};
+
+// Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
+// The candidates cut the longest sequence into 1 .. 64 parts; partial results
+// must fit the work buffer.
 template <class Seq>
-int32_t attend_chunk(const hikv_cache* c, const Seq* sq, int nseq, int64_t total) {
-    constexpr double kItemSteps = 3.0, kJoinSteps = 4.0;
-    const int64_t maxsteps = ceil_div(sq[0].n, kTcKeys);
+int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const Seq* sq, int nseq, int64_t total) {
+    const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = (int64_t)k.resident * c->sm_count;
     int64_t base_items = 0;
-    for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + kTcRows - 1) / kTcRows) * c->Hkv;
-    if (base_items >= 4 * (int64_t)c->sm_count) return INT32_MAX;
+    for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows) * c->Hkv;
+    if (base_items >= 4 * slots) return INT32_MAX;
     const int64_t room = (int64_t)c->units * c->cap * c->G;   // floats of the work buffer
     double best = 0;
     int32_t best_chunk = INT32_MAX;
     int64_t last = 0;
-    for (int k = 1; k <= 64; ++k) {
-        const int64_t ct = (maxsteps + k - 1) / k;   // key tiles per split
-        if (ct == last || (k > 1 && ct < 2)) continue;
+    for (int parts = 1; parts <= 64; ++parts) {
+        const int64_t ct = (maxsteps + parts - 1) / parts;   // steps per split
+        if (ct == last || (parts > 1 && ct < 2)) continue;
         last = ct;
         const int64_t splits = (maxsteps + ct - 1) / ct;
         if (splits > 1 && splits * total * c->Hq * (c->d + 2) > room) break;
         int64_t items = 0;
         double steps = 0, longest = 0;
         for (int i = 0; i < nseq; ++i) {
-            const int64_t tiles = ((int64_t)sq[i].nq * c->G + kTcRows - 1) / kTcRows;
+            const int64_t tiles = ((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows;
             for (int64_t t = 0; t < tiles; ++t) {
-                const int64_t seen = sq[i].n - sq[i].nq + std::min<int64_t>(sq[i].nq, (t + 1) * kTcRows / c->G);
-                const int64_t st = (seen + kTcKeys - 1) / kTcKeys;
+                const int64_t seen = sq[i].n - sq[i].nq + std::min<int64_t>(sq[i].nq, (t + 1) * k.rows / c->G);
+                const int64_t st = (seen + k.keys - 1) / k.keys;
                 items += (st + ct - 1) / ct * c->Hkv;
                 steps += (double)st * c->Hkv;
                 longest = std::max(longest, (double)std::min(st, ct));
             }
         }
-        double cost = std::max((steps + items * kItemSteps) / c->sm_count, longest + kItemSteps);
-        if (items > c->sm_count) cost += 0.5 * longest;
-        if (splits > 1) cost += kJoinSteps;
-        if (k == 1 || cost < best) {
+        double cost = std::max((steps + items * k.item_steps) / slots, longest + k.item_steps);
+        if (items > slots) cost += 0.5 * longest;
+        if (splits > 1) cost += k.join_steps;
+        if (parts == 1 || cost < best) {
             best = cost;
-            best_chunk = splits > 1 ? (int32_t)(ct * kTcKeys) : INT32_MAX;
+            best_chunk = splits > 1 ? (int32_t)(ct * k.keys) : INT32_MAX;
         }
     }
     return best_chunk;
@@ -266,14 +274,14 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
             seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
         }
     std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
-    const int rows = tc ? kTcRows : kSimtRows;
+    const ItemShape& shape = tc ? kTcShape : kSimtShape;
     for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const Seq* sq = seqs.data() + s0;
-        a.chunk = tc ? attend_chunk(c, sq, a.nseq, total) : INT32_MAX;
+        a.chunk = attend_chunk(c, shape, sq, a.nseq, total);
         int64_t items = 0, split_tokens = 0, splits_max = 0;
         for (int i = 0; i < a.nseq; ++i) {
-            const int64_t tiles = ((int64_t)sq[i].nq * c->G + rows - 1) / rows;
+            const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;
             const int64_t splits = ((int64_t)sq[i].n + a.chunk - 1) / a.chunk;
             a.brow[i] = sq[i].brow;
             a.start[i] = sq[i].start;
@@ -293,7 +301,7 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
                            : launch_attend_simt(a, c->d, (cudaStream_t)stream);
         c->launches += 1;
         if (e == cudaSuccess && split_tokens > 0) {
-            e = launch_attend_join(a, c->d, (cudaStream_t)stream);
+            e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);
             c->launches += 1;
         }
         if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");

@@ -7,14 +7,17 @@
 //
 // A CTA of 16 x 16 threads takes 64 query rows -- row = token * G + head of
 // the group, so the G heads that share a KV head share its tiles -- against
-// tiles of 64 keys staged in shared memory as fp32; a thread forms 4 x 4
-// logits and 4 x D/16 outputs, all sums in fp32.
+// tiles of 64 keys staged in shared memory; a thread forms 4 x 4 logits and
+// 4 x D/16 outputs with packed pairs of fp32 multiply-adds, all sums in
+// fp32.  Bound by the fp32 pipes and the shared-memory reads that feed them;
+// two CTAs share an SM, for which P lies over K.  With few
+// rows the keys are split over CTAs (chunk) and the parts joined.
 #include "hikv_internal.cuh"
 
 namespace hikv {
 namespace {
 
-constexpr int kBM = kSimtRows, kBN = 64, kThreads = 256;
+constexpr int kBM = kSimtRows, kBN = kSimtKeys, kThreads = 256;
 
 template <int D>
 struct Simt {
@@ -22,14 +25,19 @@ struct Simt {
     static constexpr int LP = kBN + 4;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + kBM * LD;
+    static constexpr int OFF_P = OFF_K;     // over K, which is read before P is written
     static constexpr int OFF_V = OFF_K + kBN * LD;
-    static constexpr int OFF_P = OFF_V + kBN * D;
-    static constexpr int FLOATS = OFF_P + kBM * LP;
+    static constexpr int FLOATS = OFF_V + kBN * D;
+    static_assert(LD >= LP, "P fits over K");
 };
 
+__device__ __forceinline__ float2 lo(const float4& x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi(const float4& x) { return make_float2(x.z, x.w); }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_constant__ AttendArgs a) {
     using C = Simt<D>;
+    constexpr int NV = D / 64;   // 16-byte column groups of a thread
     extern __shared__ float sm[];
     float* Qs = sm + C::OFF_Q;
     float* Ks = sm + C::OFF_K;
@@ -41,8 +49,10 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
     griddep_wait();
     const int32_t i0 = prefix_find(a.item0, a.nseq, blockIdx.x);
     const int32_t nq = a.nq[i0], first = a.start[i0];
-    const int32_t g = (blockIdx.x - a.item0[i0]) % v.hkv;
-    const int32_t tile = (a.item0[i0 + 1] - 1 - (int32_t)blockIdx.x) / v.hkv;   // the last one first
+    const int32_t rows = nq << a.gshift, tiles = ceil_div(rows, kBM);
+    const int32_t splits = (a.item0[i0 + 1] - a.item0[i0]) / (tiles * v.hkv);
+    const int32_t rem = blockIdx.x - a.item0[i0], g = rem % v.hkv, split = rem / v.hkv % splits;
+    const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * kBM;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i0] * v.hkv + g;
     const int32_t n = v.len[u];
     if (n < nq || n > v.cap) {
@@ -50,43 +60,43 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
         return;
     }
     const int32_t G = 1 << a.gshift;
-    const int64_t rows = (int64_t)nq << a.gshift;
-    const int64_t r0 = (int64_t)tile * kBM;
     const int32_t seen0 = n - nq;   // slots before the first query's own
+    const int32_t first_lim = seen0 + (r0 >> a.gshift);                            // slots [0, lim] are seen by the
+    const int32_t last_lim = seen0 + ((min(r0 + kBM, rows) - 1) >> a.gshift);      // first and the last row
+    const int32_t lo_slot = splits > 1 ? split * a.chunk : 0;
+    const int32_t end = splits > 1 ? min(last_lim + 1, lo_slot + a.chunk) : last_lim + 1;
+    if (lo_slot >= end) return;
 
     for (int i = tid; i < kBM * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r0 + r < rows) {
-            const int32_t t = first + (int32_t)((r0 + r) >> a.gshift), h = (g << a.gshift) + (int32_t)((r0 + r) & (G - 1));
+            const int32_t t = first + ((r0 + r) >> a.gshift), h = (g << a.gshift) + ((r0 + r) & (G - 1));
             x = *reinterpret_cast<const float4*>(a.q.row(t, h) + 4 * c);
         }
         *reinterpret_cast<float4*>(Qs + r * C::LD + c) = x;
     }
-    // the slots each of this thread's rows sees: [0, lim]
-    int32_t lim[4];
+    int32_t lim[4];   // this thread's rows see slots [0, lim]
     float m[4], l[4];
-    float4 o[4][D / 64];
+    float2 o[4][2 * NV];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + ty + 16 * i;
-        lim[i] = r < rows ? seen0 + (int32_t)(r >> a.gshift) : -1;
+        const int32_t r = r0 + ty + 16 * i;
+        lim[i] = r < rows ? seen0 + (r >> a.gshift) : -1;
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 2 * NV; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
-    const int64_t rlast = r0 + kBM < rows ? r0 + kBM - 1 : rows - 1;
-    const int32_t first_lim = seen0 + (int32_t)(r0 >> a.gshift), last_lim = seen0 + (int32_t)(rlast >> a.gshift);
 
-    for (int32_t s0 = 0; s0 <= last_lim; s0 += kBN) {
+    for (int32_t s0 = lo_slot; s0 < end; s0 += kBN) {
         __syncthreads();
         for (int i = tid; i < kBN * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (s0 + r <= last_lim) {
-                const uint8_t* kp = row_ptr(v, u, s0 + r, false);
-                const uint8_t* vp = row_ptr(v, u, s0 + r, true);
+            if (s0 + r < end) {
+                const uint8_t* kp = slot_row(v, u, s0 + r, false);
+                const uint8_t* vp = slot_row(v, u, s0 + r, true);
                 if (kp) x = *reinterpret_cast<const float4*>(kp + 4 * c);
                 if (vp) y = *reinterpret_cast<const float4*>(vp + 4 * c);
             }
@@ -94,7 +104,11 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
             *reinterpret_cast<float4*>(Vs + r * D + c) = y;
         }
         __syncthreads();
-        float s[4][4] = {};
+        float2 s2[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
             float4 q[4], k[4];
@@ -105,18 +119,18 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
+                for (int j = 0; j < 4; ++j) s2[i][j] = ffma2(hi(q[i]), hi(k[j]), ffma2(lo(q[i]), lo(k[j]), s2[i][j]));
         }
-        const bool edge = s0 + kBN - 1 > first_lim;   // some row does not see the whole tile
+        __syncthreads();   // K is read: P may lie over it
+        const bool edge = s0 + kBN - 1 > first_lim || s0 + kBN > end;   // some row does not see the whole tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float mx = m[i];
+            float mx = m[i], s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] *= a.qscale;
-                if (edge && s0 + tx + 16 * j > lim[i]) s[i][j] = -INFINITY;
-                mx = fmaxf(mx, s[i][j]);
+                s[j] = (s2[i][j].x + s2[i][j].y) * a.qscale;
+                if (edge && (s0 + tx + 16 * j > lim[i] || s0 + tx + 16 * j >= end)) s[j] = -INFINITY;
+                mx = fmaxf(mx, s[j]);
             }
 #pragma unroll
             for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -126,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(s[i][j] - base);
+                const float p = exp2f(s[j] - base);
                 sum += p;
                 Ps[(ty + 16 * i) * C::LP + tx + 16 * j] = p;
             }
@@ -134,44 +148,70 @@ __global__ void __launch_bounds__(kThreads) k_attend_simt(const __grid_constant_
             for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             l[i] = l[i] * f + sum;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
+            for (int j = 0; j < 2 * NV; ++j) {
                 o[i][j].x *= f;
                 o[i][j].y *= f;
-                o[i][j].z *= f;
-                o[i][j].w *= f;
             }
         }
         __syncwarp();   // a row's probabilities are written and read by the same half warp
-        for (int k = 0; k < kBN; ++k) {
-            float4 x[D / 64];
+        if (!edge) {
+#pragma unroll 2
+            for (int k = 0; k < kBN; k += 4) {
+                float4 p[4];
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) x[j] = *reinterpret_cast<const float4*>(Vs + k * D + tx * 4 + 64 * j);
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * C::LP + k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // at the edge a row skips the values it does not see: 0 x inf is not 0
-                if (edge && s0 + k > lim[i]) continue;
-                const float p = Ps[(ty + 16 * i) * C::LP + k];
+                for (int kk = 0; kk < 4; ++kk) {
+                    float4 x[NV];
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    o[i][j].x = fmaf(p, x[j].x, o[i][j].x);
-                    o[i][j].y = fmaf(p, x[j].y, o[i][j].y);
-                    o[i][j].z = fmaf(p, x[j].z, o[i][j].z);
-                    o[i][j].w = fmaf(p, x[j].w, o[i][j].w);
+                    for (int j = 0; j < NV; ++j)
+                        x[j] = *reinterpret_cast<const float4*>(Vs + (k + kk) * D + tx * 4 + 64 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y = kk == 0 ? p[i].x : (kk == 1 ? p[i].y : (kk == 2 ? p[i].z : p[i].w));
+                        const float2 y2 = make_float2(y, y);
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            o[i][2 * j] = ffma2(y2, lo(x[j]), o[i][2 * j]);
+                            o[i][2 * j + 1] = ffma2(y2, hi(x[j]), o[i][2 * j + 1]);
+                        }
+                    }
+                }
+            }
+        } else {
+            // a row skips the values it does not see: 0 x inf is not 0
+            const int32_t kn = min(kBN, end - s0);
+            for (int k = 0; k < kn; ++k) {
+                float4 x[NV];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) x[j] = *reinterpret_cast<const float4*>(Vs + k * D + tx * 4 + 64 * j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (s0 + k > lim[i]) continue;
+                    const float y = Ps[(ty + 16 * i) * C::LP + k];
+                    const float2 y2 = make_float2(y, y);
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        o[i][2 * j] = ffma2(y2, lo(x[j]), o[i][2 * j]);
+                        o[i][2 * j + 1] = ffma2(y2, hi(x[j]), o[i][2 * j + 1]);
+                    }
                 }
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + ty + 16 * i;
+        const int32_t r = r0 + ty + 16 * i;
         if (r >= rows) continue;
-        const int32_t t = first + (int32_t)(r >> a.gshift), h = (g << a.gshift) + (int32_t)(r & (G - 1));
-        float* dst = reinterpret_cast<float*>(a.out.row(t, h));
-        const float inv = 1.0f / l[i];
+        const int32_t t = first + (r >> a.gshift), h = (g << a.gshift) + (r & (G - 1));
+        const int64_t pr = (int64_t)split * a.part_rows + (int64_t)t * v.hq + h;
+        const float f = splits > 1 ? 1.f : 1.0f / l[i];
+        float* dst = splits > 1 ? a.part + pr * D : reinterpret_cast<float*>(a.out.row(t, h));
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
+        for (int j = 0; j < NV; ++j)
             *reinterpret_cast<float4*>(dst + tx * 4 + 64 * j) =
-                make_float4(o[i][j].x * inv, o[i][j].y * inv, o[i][j].z * inv, o[i][j].w * inv);
+                make_float4(o[i][2 * j].x * f, o[i][2 * j].y * f, o[i][2 * j + 1].x * f, o[i][2 * j + 1].y * f);
+        if (splits > 1 && tx == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m[i], l[i]);
     }
 }
 

@@ -1,5 +1,5 @@
 // Causal attention of packed queries over the paged cache on the tensor cores
-// (bf16), and the join of split results.
+// (bf16).
 //
 //   o_i = sum_{s <= lim_i} 2^(t_is - m_i) v_s / sum_{s <= lim_i} 2^(t_is - m_i),
 //   t_is = scale log2(e) q_i . k_s,
@@ -818,41 +818,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Join the splits of every query row: warp per row (t, h) of the sequences
-// whose keys were split.  With m the largest of the partial maxima,
-// o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
-template <int D>
-__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a) {
-    const View& v = a.v;
-    griddep_launch_dependents();
-    griddep_wait();
-    const int32_t x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int32_t tok = x / v.hq, h = x % v.hq;
-    if (tok >= a.comb0[a.nseq]) return;
-    const int32_t i = prefix_find(a.comb0, a.nseq, tok);
-    const int32_t j = tok - a.comb0[i];
-    const int32_t n = v.len[a.u0 + a.brow[i] * v.hkv + (h >> a.gshift)];
-    const int32_t lim = n - a.nq[i] + j;
-    if (lim < 0 || n > v.cap) return;
-    const int32_t ns = lim / a.chunk + 1;
-    const int64_t row = (int64_t)(a.start[i] + j) * v.hq + h;
-    float m = -INFINITY;
-    for (int32_t s = 0; s < ns; ++s) m = fmaxf(m, a.part_ml[(s * a.part_rows + row) * 2]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[D / 32] = {};
-    for (int32_t s = 0; s < ns; ++s) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * a.part_rows + row) * 2);
-        const float f = exp2f(ml.x - base);
-        l = fmaf(f, ml.y, l);
-        const float* p = a.part + (s * a.part_rows + row) * D + lane * (D / 32);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[k] = fmaf(f, p[k], o[k]);
-    }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out.row(a.start[i] + j, h)) + lane * (D / 64);
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) dst[k] = pack_bf16x2(o[2 * k] / l, o[2 * k + 1] / l);
-}
-
 template <int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, cudaStream_t s) {
     const void* f = (const void*)k_attend_tc<D>;
@@ -866,12 +831,6 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
                              cudaStream_t s) {
     return d == 128 ? launch<128>(a, qmap, kvmap, s) : launch<64>(a, qmap, kvmap, s);
-}
-
-cudaError_t launch_attend_join(const AttendArgs& a, int d, cudaStream_t s) {
-    const int32_t grid = (int32_t)(((int64_t)a.comb0[a.nseq] * a.v.hq + 3) / 4);
-    return d == 128 ? launch_overlapped(k_attend_join<128>, grid, 128, 0, s, a)
-                    : launch_overlapped(k_attend_join<64>, grid, 128, 0, s, a);
 }
 
 }  // namespace hikv
