@@ -667,6 +667,7 @@ struct AttendArgs {
     float* part;            // partial results of split items: [splits][part_rows][d] outputs, ...
     float* part_ml;         // ... [splits][part_rows][2] maxima and sums
     int64_t part_rows;      // rows (t, h) of the packed batch
+    int32_t splits;         // the most parts a sequence's keys are split into
     int32_t nseq, items;
     int32_t brow[kAttSeqs];        // batch row
     int32_t start[kAttSeqs];       // first packed row

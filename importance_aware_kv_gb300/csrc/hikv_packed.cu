@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <new>
 #include <vector>
 
 #include "hikv_cache.cuh"
@@ -96,6 +97,80 @@ int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const Seq* sq, int
         }
     }
     return best_chunk;
+}
+
+// The launches of hikv_attend_packed, its arguments checked.
+hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t total, const hikv_rows* q,
+                          const hikv_rows* out, hikv_stream_t stream) {
+    DeviceGuard guard(c->device);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
+    pdl_forget(c);
+    const bool tc = c->dtype == HIKV_BF16;
+    CUtensorMap qmap;
+    if (tc) {
+        // q as [tokens][heads][d], boxes of 128 query rows x 128 bytes
+        cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->Hq, (cuuint64_t)total};
+        cuuint64_t strides[2] = {(cuuint64_t)(c->Hq > 1 ? q->head_stride : c->d) * 2,
+                                 (cuuint64_t)(total > 1 ? q->token_stride : c->d) * 2};
+        cuuint32_t box[3] = {64u, (cuuint32_t)c->G, (cuuint32_t)(128 / c->G)};
+        cuuint32_t estr[3] = {1u, 1u, 1u};
+        const CUresult r = tensor_map_encoder()(
+            &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: no tensor map of q (%d)", (int)r);
+    }
+    AttendArgs a{};
+    a.v = c->v;
+    a.u0 = u0;
+    while ((1 << a.gshift) < c->G) ++a.gshift;
+    a.q = rows_arg(c, q);
+    a.out = rows_arg(c, out);
+    a.qscale = c->scale * 1.4426950408889634f;
+    a.part_rows = total * c->Hq;
+    // the sequences with queries, longest first: the work items start with the heaviest
+    struct Seq { int32_t brow, start, nq, n; };
+    std::vector<Seq> seqs;
+    for (int b = 0, row = 0; b < c->B; row += nq[b++])
+        if (nq[b] > 0) {
+            const int32_t* len = c->len.data() + u0 + b * c->Hkv;
+            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
+        }
+    std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
+    const ItemShape& shape = tc ? kTcShape : kSimtShape;
+    for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
+        a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
+        const Seq* sq = seqs.data() + s0;
+        a.chunk = attend_chunk(c, shape, sq, a.nseq, total);
+        int64_t items = 0, split_tokens = 0, splits_max = 0;
+        for (int i = 0; i < a.nseq; ++i) {
+            const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;
+            const int64_t splits = ((int64_t)sq[i].n + a.chunk - 1) / a.chunk;
+            a.brow[i] = sq[i].brow;
+            a.start[i] = sq[i].start;
+            a.nq[i] = sq[i].nq;
+            a.item0[i] = (int32_t)items;
+            a.comb0[i] = (int32_t)split_tokens;
+            items += tiles * splits * c->Hkv;
+            split_tokens += splits > 1 ? sq[i].nq : 0;
+            splits_max = std::max(splits_max, splits);
+        }
+        if (items > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
+        a.item0[a.nseq] = a.items = (int32_t)items;
+        a.comb0[a.nseq] = (int32_t)split_tokens;
+        a.splits = (int32_t)splits_max;
+        a.part = c->d_logits;
+        a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
+        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
+                           : launch_attend_simt(a, c->d, (cudaStream_t)stream);
+        c->launches += 1;
+        if (e == cudaSuccess && split_tokens > 0) {
+            e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);
+            c->launches += 1;
+        }
+        if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");
+    }
+    return HIKV_OK;
 }
 
 }  // namespace
@@ -229,6 +304,7 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
     const int64_t total = packed_total(c, nq);
     if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: a query count is negative or their sum too large");
     if (total == 0) return HIKV_OK;
+    if (total * c->Hq > INT32_MAX / 2) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
     const char* bad = nullptr;
     if ((bad = rows_fault(c, q, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
     if ((bad = rows_fault(c, out, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out has %s", bad);
@@ -238,75 +314,11 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
         if (nq[i / c->Hkv] > c->tail[u0 + i])
             return fail(HIKV_ERR_STATE, "attend_packed: %d queries of unit %d, which holds its newest %d in order",
                         nq[i / c->Hkv], u0 + i, c->tail[u0 + i]);
-    DeviceGuard guard(c->device);
-    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
-    pdl_forget(c);
-    if (total * c->Hq > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
-    const bool tc = c->dtype == HIKV_BF16;
-    CUtensorMap qmap;
-    if (tc) {
-        // q as [tokens][heads][d], boxes of 128 query rows x 128 bytes
-        cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->Hq, (cuuint64_t)total};
-        cuuint64_t strides[2] = {(cuuint64_t)(c->Hq > 1 ? q->head_stride : c->d) * 2,
-                                 (cuuint64_t)(total > 1 ? q->token_stride : c->d) * 2};
-        cuuint32_t box[3] = {64u, (cuuint32_t)c->G, (cuuint32_t)(128 / c->G)};
-        cuuint32_t estr[3] = {1u, 1u, 1u};
-        const CUresult r = tensor_map_encoder()(
-            &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: no tensor map of q (%d)", (int)r);
+    try {
+        return attend_launch(c, u0, nq, total, q, out, stream);
+    } catch (const std::bad_alloc&) {
+        return fail(HIKV_ERR_OUT_OF_MEMORY, "attend_packed: host memory");
     }
-    AttendArgs a{};
-    a.v = c->v;
-    a.u0 = u0;
-    while ((1 << a.gshift) < c->G) ++a.gshift;
-    a.q = rows_arg(c, q);
-    a.out = rows_arg(c, out);
-    a.qscale = c->scale * 1.4426950408889634f;
-    a.part_rows = total * c->Hq;
-    // the sequences with queries, longest first: the work items start with the heaviest
-    struct Seq { int32_t brow, start, nq, n; };
-    std::vector<Seq> seqs;
-    for (int b = 0, row = 0; b < c->B; row += nq[b++])
-        if (nq[b] > 0) {
-            const int32_t* len = c->len.data() + u0 + b * c->Hkv;
-            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
-        }
-    std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
-    const ItemShape& shape = tc ? kTcShape : kSimtShape;
-    for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
-        a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
-        const Seq* sq = seqs.data() + s0;
-        a.chunk = attend_chunk(c, shape, sq, a.nseq, total);
-        int64_t items = 0, split_tokens = 0, splits_max = 0;
-        for (int i = 0; i < a.nseq; ++i) {
-            const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;
-            const int64_t splits = ((int64_t)sq[i].n + a.chunk - 1) / a.chunk;
-            a.brow[i] = sq[i].brow;
-            a.start[i] = sq[i].start;
-            a.nq[i] = sq[i].nq;
-            a.item0[i] = (int32_t)items;
-            a.comb0[i] = (int32_t)split_tokens;
-            items += tiles * splits * c->Hkv;
-            split_tokens += splits > 1 ? sq[i].nq : 0;
-            splits_max = std::max(splits_max, splits);
-        }
-        if (items > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
-        a.item0[a.nseq] = a.items = (int32_t)items;
-        a.comb0[a.nseq] = (int32_t)split_tokens;
-        a.part = c->d_logits;
-        a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
-        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
-                           : launch_attend_simt(a, c->d, (cudaStream_t)stream);
-        c->launches += 1;
-        if (e == cudaSuccess && split_tokens > 0) {
-            e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);
-            c->launches += 1;
-        }
-        if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");
-    }
-    return HIKV_OK;
 }
 
 hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* ndrop, hikv_stream_t stream) {

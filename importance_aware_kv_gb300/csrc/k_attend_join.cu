@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     const int32_t n = v.len[a.u0 + a.brow[i] * v.hkv + (h >> a.gshift)];
     const int32_t lim = n - a.nq[i] + j;   // the row sees slots [0, lim]
     if (lim < 0 || n > v.cap) return;
-    const int32_t ns = lim / a.chunk + 1;
+    const int32_t ns = min(lim / a.chunk + 1, a.splits);
     const int64_t row = (int64_t)(a.start[i] + j) * v.hq + h;
     float m = -INFINITY;
     for (int32_t s = lane; s < ns; s += 32) m = fmaxf(m, a.part_ml[(s * a.part_rows + row) * 2]);

@@ -23,13 +23,25 @@ template <int D>
 struct Simt {
     static constexpr int LD = D + 4;        // row strides that spread the banks of 16-byte reads
     static constexpr int LP = kBN + 4;
+    static constexpr int BUFS = D == 64 ? 2 : 1;   // tiles of K and V: the next one loads under this one's work
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + kBM * LD;
-    static constexpr int OFF_P = OFF_K;     // over K, which is read before P is written
-    static constexpr int OFF_V = OFF_K + kBN * LD;
-    static constexpr int FLOATS = OFF_V + kBN * D;
+    static constexpr int OFF_V = OFF_K + BUFS * kBN * LD;
+    // P lies over K (which is read before P is written) where K has one buffer
+    static constexpr int OFF_P = BUFS == 1 ? OFF_K : OFF_V + BUFS * kBN * D;
+    static constexpr int FLOATS = OFF_V + BUFS * kBN * D + (BUFS == 1 ? 0 : kBM * LP);
     static_assert(LD >= LP, "P fits over K");
 };
+
+// 16 bytes global -> shared without a register, or zeros
+__device__ __forceinline__ void copy16(float* dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the N newest groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ float2 lo(const float4& x) { return make_float2(x.x, x.y); }
 __device__ __forceinline__ float2 hi(const float4& x) { return make_float2(x.z, x.w); }
@@ -89,20 +101,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         for (int j = 0; j < 2 * NV; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
 
-    for (int32_t s0 = lo_slot; s0 < end; s0 += kBN) {
-        __syncthreads();
-        for (int i = tid; i < kBN * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (s0 + r < end) {
-                const uint8_t* kp = slot_row(v, u, s0 + r, false);
-                const uint8_t* vp = slot_row(v, u, s0 + r, true);
-                if (kp) x = *reinterpret_cast<const float4*>(kp + 4 * c);
-                if (vp) y = *reinterpret_cast<const float4*>(vp + 4 * c);
+    // queue the keys, then the values of the tile at s0; rows past `end` are zero
+    auto queue = [&](int32_t s0, int buf) {
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            float* dst = is_v ? Vs + buf * kBN * D : Ks + buf * kBN * C::LD;
+#pragma unroll 4
+            for (int i = tid; i < kBN * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), c = i % (D / 4) * 4;
+                float* x = dst + r * (is_v ? D : C::LD) + c;
+                const uint8_t* row = s0 + r < end ? slot_row(v, u, s0 + r, is_v) : nullptr;
+                if (row) copy16(x, row + 4 * c);
+                else *reinterpret_cast<float4*>(x) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            *reinterpret_cast<float4*>(Ks + r * C::LD + c) = x;
-            *reinterpret_cast<float4*>(Vs + r * D + c) = y;
+            copy_commit();
         }
+    };
+    if (C::BUFS == 2) queue(lo_slot, 0);
+    int buf = 0;
+    for (int32_t s0 = lo_slot; s0 < end; s0 += kBN, buf ^= C::BUFS - 1) {
+        __syncthreads();   // the tile before is done with
+        if (C::BUFS == 2) {
+            if (s0 + kBN < end) {
+                queue(s0 + kBN, buf ^ 1);
+                copy_wait<3>();
+            } else {
+                copy_wait<1>();
+            }
+        } else {
+            queue(s0, 0);
+            copy_wait<1>();
+        }
+        const float* Kt = Ks + buf * kBN * C::LD;
+        const float* Vt = Vs + buf * kBN * D;
         __syncthreads();
         float2 s2[4][4];
 #pragma unroll
@@ -115,13 +145,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * C::LD + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * C::LD + c);
+            for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(Kt + (tx + 16 * j) * C::LD + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s2[i][j] = ffma2(hi(q[i]), hi(k[j]), ffma2(lo(q[i]), lo(k[j]), s2[i][j]));
         }
-        __syncthreads();   // K is read: P may lie over it
+        // the values are there; and K is read: P may lie over it
+        if (C::BUFS == 2 && s0 + kBN < end) copy_wait<2>();
+        else copy_wait<0>();
+        __syncthreads();
         const bool edge = s0 + kBN - 1 > first_lim || s0 + kBN > end;   // some row does not see the whole tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -165,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
                     float4 x[NV];
 #pragma unroll
                     for (int j = 0; j < NV; ++j)
-                        x[j] = *reinterpret_cast<const float4*>(Vs + (k + kk) * D + tx * 4 + 64 * j);
+                        x[j] = *reinterpret_cast<const float4*>(Vt + (k + kk) * D + tx * 4 + 64 * j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float y = kk == 0 ? p[i].x : (kk == 1 ? p[i].y : (kk == 2 ? p[i].z : p[i].w));
@@ -184,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
             for (int k = 0; k < kn; ++k) {
                 float4 x[NV];
 #pragma unroll
-                for (int j = 0; j < NV; ++j) x[j] = *reinterpret_cast<const float4*>(Vs + k * D + tx * 4 + 64 * j);
+                for (int j = 0; j < NV; ++j) x[j] = *reinterpret_cast<const float4*>(Vt + k * D + tx * 4 + 64 * j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (s0 + k > lim[i]) continue;

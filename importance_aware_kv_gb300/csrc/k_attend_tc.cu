@@ -386,8 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();   // what the kernel before writes is there: lengths, pages, q
     Item w0;
     if (warp == 8) {
-        // (a wait gave up in this launch or before: start nothing more)
-        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(v.err) & DEVERR_TIMEOUT;
+        // (a wait of this kernel gave up: start nothing more, each item would wait as long)
+        const volatile uint32_t* err = v.err;
+        const bool bad = (err[0] & DEVERR_TIMEOUT) != 0 && err[1] == kWaitAttend;
         if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
         w0.some = !bad;
     }
