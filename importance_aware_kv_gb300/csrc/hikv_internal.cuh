@@ -685,8 +685,9 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
     }
     return lo;
 }
-cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s);
-constexpr int kSimtRows = 64;   // query rows of a work item of that kernel
+// `rows`: query rows of a work item, kSimtRows or, for calls with little work, kSimtFewRows
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, int rows, cudaStream_t s);
+constexpr int kSimtRows = 64, kSimtFewRows = 32;
 constexpr int kSimtKeys = 64;   // keys per tile
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
                              cudaStream_t s);

@@ -56,6 +56,7 @@ struct ItemShape {
 };
 constexpr ItemShape kTcShape{kTcRows, kTcKeys, 1, 3.0, 4.0};
 constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 1.0, 2.0};
+constexpr ItemShape kSimtFewShape{kSimtFewRows, kSimtKeys, 2, 1.0, 3.0};
 
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
 // The candidates cut the longest sequence into 1 .. 64 parts; partial results
@@ -137,7 +138,9 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
         }
     std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
-    const ItemShape& shape = tc ? kTcShape : kSimtShape;
+    int64_t large = 0;   // work items of the CUDA-core kernel's larger shape
+    for (const Seq& x : seqs) large += (((int64_t)x.nq * c->G + kSimtRows - 1) / kSimtRows) * c->Hkv;
+    const ItemShape& shape = tc ? kTcShape : (large >= 2 * c->sm_count ? kSimtShape : kSimtFewShape);
     for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const Seq* sq = seqs.data() + s0;
@@ -162,7 +165,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.part = c->d_logits;
         a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
         cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
-                           : launch_attend_simt(a, c->d, (cudaStream_t)stream);
+                           : launch_attend_simt(a, c->d, shape.rows, (cudaStream_t)stream);
         c->launches += 1;
         if (e == cudaSuccess && split_tokens > 0) {
             e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);

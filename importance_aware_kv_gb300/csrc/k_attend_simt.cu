@@ -9,28 +9,33 @@
 // the group, so the G heads that share a KV head share its tiles -- against
 // tiles of 64 keys staged in shared memory; a thread forms 4 x 4 logits and
 // 4 x D/16 outputs with packed pairs of fp32 multiply-adds, all sums in
-// fp32.  Bound by the fp32 pipes and the shared-memory reads that feed them;
-// two CTAs share an SM, for which P lies over K.  With few
-// rows the keys are split over CTAs (chunk) and the parts joined.
+// fp32.  Calls too small to give every SM two such CTAs take 32 rows, 2 x 4
+// logits a thread (prompts of 256, 100, 511 and 1 tokens with 4/2 heads, d =
+// 64: 50 -> 43 us; five drafted tokens over eight 16K caches with 32/8 heads,
+// d = 128: 827 -> 634 us).  Bound by the latency between shared-memory reads
+// and the fp32 pipes they feed (4096 tokens with 32/8 heads, d = 128: 2.95 ms,
+// 46.6 TFLOP/s); two CTAs share an SM, for which P lies over K at d = 128.
+// K and V come by asynchronous copies, at d = 64 a tile ahead.  With few rows
+// the keys are split over CTAs (chunk) and the parts joined.
 #include "hikv_internal.cuh"
 
 namespace hikv {
 namespace {
 
-constexpr int kBM = kSimtRows, kBN = kSimtKeys, kThreads = 256;
+constexpr int kBN = kSimtKeys, kThreads = 256;
 
-template <int D>
+template <int D, int BM>
 struct Simt {
     static constexpr int LD = D + 4;        // row strides that spread the banks of 16-byte reads
     static constexpr int LP = kBN + 4;
     static constexpr int BUFS = D == 64 ? 2 : 1;   // tiles of K and V: the next one loads under this one's work
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + kBM * LD;
+    static constexpr int OFF_K = OFF_Q + BM * LD;
     static constexpr int OFF_V = OFF_K + BUFS * kBN * LD;
     // P lies over K (which is read before P is written) where K has one buffer
     static constexpr int OFF_P = BUFS == 1 ? OFF_K : OFF_V + BUFS * kBN * D;
-    static constexpr int FLOATS = OFF_V + BUFS * kBN * D + (BUFS == 1 ? 0 : kBM * LP);
-    static_assert(LD >= LP, "P fits over K");
+    static constexpr int FLOATS = OFF_V + BUFS * kBN * D + (BUFS == 1 ? 0 : BM * LP);
+    static_assert(LD >= LP && BM <= kBN, "P fits over K");
 };
 
 // 16 bytes global -> shared without a register, or zeros
@@ -46,9 +51,10 @@ __device__ __forceinline__ void copy_wait() {   // all but the N newest groups h
 __device__ __forceinline__ float2 lo(const float4& x) { return make_float2(x.x, x.y); }
 __device__ __forceinline__ float2 hi(const float4& x) { return make_float2(x.z, x.w); }
 
-template <int D>
+template <int D, int BM>
 __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_constant__ AttendArgs a) {
-    using C = Simt<D>;
+    using C = Simt<D, BM>;
+    constexpr int R = BM / 16;   // rows of a thread
     constexpr int NV = D / 64;   // 16-byte column groups of a thread
     extern __shared__ float sm[];
     float* Qs = sm + C::OFF_Q;
@@ -61,10 +67,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
     griddep_wait();
     const int32_t i0 = prefix_find(a.item0, a.nseq, blockIdx.x);
     const int32_t nq = a.nq[i0], first = a.start[i0];
-    const int32_t rows = nq << a.gshift, tiles = ceil_div(rows, kBM);
+    const int32_t rows = nq << a.gshift, tiles = ceil_div(rows, BM);
     const int32_t splits = (a.item0[i0 + 1] - a.item0[i0]) / (tiles * v.hkv);
     const int32_t rem = blockIdx.x - a.item0[i0], g = rem % v.hkv, split = rem / v.hkv % splits;
-    const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * kBM;   // the last rows, which see most, first
+    const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * BM;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i0] * v.hkv + g;
     const int32_t n = v.len[u];
     if (n < nq || n > v.cap) {
@@ -74,12 +80,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
     const int32_t G = 1 << a.gshift;
     const int32_t seen0 = n - nq;   // slots before the first query's own
     const int32_t first_lim = seen0 + (r0 >> a.gshift);                            // slots [0, lim] are seen by the
-    const int32_t last_lim = seen0 + ((min(r0 + kBM, rows) - 1) >> a.gshift);      // first and the last row
+    const int32_t last_lim = seen0 + ((min(r0 + BM, rows) - 1) >> a.gshift);      // first and the last row
     const int32_t lo_slot = splits > 1 ? split * a.chunk : 0;
     const int32_t end = splits > 1 ? min(last_lim + 1, lo_slot + a.chunk) : last_lim + 1;
     if (lo_slot >= end) return;
 
-    for (int i = tid; i < kBM * (D / 4); i += kThreads) {
+    for (int i = tid; i < BM * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r0 + r < rows) {
@@ -88,11 +94,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         }
         *reinterpret_cast<float4*>(Qs + r * C::LD + c) = x;
     }
-    int32_t lim[4];   // this thread's rows see slots [0, lim]
-    float m[4], l[4];
-    float2 o[4][2 * NV];
+    int32_t lim[R];   // this thread's rows see slots [0, lim]
+    float m[R], l[R];
+    float2 o[R][2 * NV];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int32_t r = r0 + ty + 16 * i;
         lim[i] = r < rows ? seen0 + (r >> a.gshift) : -1;
         m[i] = -INFINITY;
@@ -103,18 +109,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
 
     // queue the keys, then the values of the tile at s0; rows past `end` are zero
     auto queue = [&](int32_t s0, int buf) {
-        for (int is_v = 0; is_v < 2; ++is_v) {
-            float* dst = is_v ? Vs + buf * kBN * D : Ks + buf * kBN * C::LD;
-#pragma unroll 4
-            for (int i = tid; i < kBN * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), c = i % (D / 4) * 4;
-                float* x = dst + r * (is_v ? D : C::LD) + c;
-                const uint8_t* row = s0 + r < end ? slot_row(v, u, s0 + r, is_v) : nullptr;
-                if (row) copy16(x, row + 4 * c);
-                else *reinterpret_cast<float4*>(x) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            copy_commit();
+        constexpr int PER = kBN * (D / 4) / kThreads;   // 16-byte pieces of a thread, in as many rows
+        const int c = tid % (D / 4) * 4, r0t = tid / (D / 4);
+        const int64_t to_v = (int64_t)v.page_tokens * v.row_bytes;
+        const uint8_t* row[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = r0t + i * (kBN / PER);
+            float* x = Ks + buf * kBN * C::LD + r * C::LD + c;
+            row[i] = s0 + r < end ? slot_row(v, u, s0 + r, false) : nullptr;
+            if (row[i]) copy16(x, row[i] + 4 * c);
+            else *reinterpret_cast<float4*>(x) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        copy_commit();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            float* x = Vs + buf * kBN * D + (r0t + i * (kBN / PER)) * D + c;
+            if (row[i]) copy16(x, row[i] + to_v + 4 * c);
+            else *reinterpret_cast<float4*>(x) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        copy_commit();
     };
     if (C::BUFS == 2) queue(lo_slot, 0);
     int buf = 0;
@@ -134,20 +148,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         const float* Kt = Ks + buf * kBN * C::LD;
         const float* Vt = Vs + buf * kBN * D;
         __syncthreads();
-        float2 s2[4][4];
+        float2 s2[R][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < D; c += 4) {
-            float4 q[4], k[4];
+            float4 q[R], k[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * C::LD + c);
+            for (int i = 0; i < R; ++i) q[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * C::LD + c);
 #pragma unroll
             for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(Kt + (tx + 16 * j) * C::LD + c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s2[i][j] = ffma2(hi(q[i]), hi(k[j]), ffma2(lo(q[i]), lo(k[j]), s2[i][j]));
         }
@@ -157,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         __syncthreads();
         const bool edge = s0 + kBN - 1 > first_lim || s0 + kBN > end;   // some row does not see the whole tile
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             float mx = m[i], s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -188,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         }
         __syncwarp();   // a row's probabilities are written and read by the same half warp
         if (!edge) {
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < kBN; k += 4) {
-                float4 p[4];
+                float4 p[R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * C::LP + k);
+                for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * C::LP + k);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     float4 x[NV];
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
                     for (int j = 0; j < NV; ++j)
                         x[j] = *reinterpret_cast<const float4*>(Vt + (k + kk) * D + tx * 4 + 64 * j);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < R; ++i) {
                         const float y = kk == 0 ? p[i].x : (kk == 1 ? p[i].y : (kk == 2 ? p[i].z : p[i].w));
                         const float2 y2 = make_float2(y, y);
 #pragma unroll
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < NV; ++j) x[j] = *reinterpret_cast<const float4*>(Vt + k * D + tx * 4 + 64 * j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < R; ++i) {
                     if (s0 + k > lim[i]) continue;
                     const float y = Ps[(ty + 16 * i) * C::LP + k];
                     const float2 y2 = make_float2(y, y);
@@ -233,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int32_t r = r0 + ty + 16 * i;
         if (r >= rows) continue;
         const int32_t t = first + (r >> a.gshift), h = (g << a.gshift) + (r & (G - 1));
@@ -248,19 +262,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
     }
 }
 
-template <int D>
+template <int D, int BM>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-    const void* f = (const void*)k_attend_simt<D>;
-    const size_t smem = Simt<D>::FLOATS * sizeof(float);
-    cudaError_t e = func_smem_optin(f, smem);
+    const size_t smem = Simt<D, BM>::FLOATS * sizeof(float);
+    const cudaError_t e = func_smem_optin((const void*)k_attend_simt<D, BM>, smem);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(k_attend_simt<D>, a.items, kThreads, smem, s, a);
+    return launch_overlapped(k_attend_simt<D, BM>, a.items, kThreads, smem, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_simt(const AttendArgs& a, int d, cudaStream_t s) {
-    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, int rows, cudaStream_t s) {
+    if (rows == kSimtRows) return d == 128 ? launch<128, kSimtRows>(a, s) : launch<64, kSimtRows>(a, s);
+    return d == 128 ? launch<128, kSimtFewRows>(a, s) : launch<64, kSimtFewRows>(a, s);
 }
 
 }  // namespace hikv
