@@ -29,6 +29,10 @@ struct hikv_cache {
     View v{};
     int32_t* d_append_base = nullptr;
     float* d_logits = nullptr;          // long-chunk decode logits (may be null)
+    // packed attention's partial results: room for every SM's three work
+    // items of 256 query rows, or for the longest unit's keys in parts of 256
+    float* d_attend = nullptr;
+    int64_t attend_room = 0;            // floats
     unsigned long long* d_cand = nullptr;
     int32_t* d_cand_slot = nullptr;
     int32_t* d_holes = nullptr;

@@ -270,6 +270,9 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
     c->asg_key.assign(c->L, 0);
     c->sasg_key.assign(c->L, 0);
     if (need_logits) ALLOC(c->d_logits, U * (size_t)c->cap * G);
+    c->attend_room = std::min<int64_t>(3LL * c->sm_count * kTcRows * (c->d + 2),
+                                       (int64_t)c->per_layer * c->cap * G * ceil_div(c->cap, 256) * (c->d + 2));
+    ALLOC(c->d_attend, (size_t)c->attend_room);
     if (c->elem) {
         c->elem_stride = std::min(c->cap, elem_max_tokens());
         const int spans = ceil_div(c->elem_stride, elem_span_ranks());

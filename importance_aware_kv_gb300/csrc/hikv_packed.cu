@@ -47,51 +47,62 @@ int64_t packed_total(const hikv_cache* c, const int32_t* ntok) {
 }
 
 // The shape of the work items of the tensor-core and of the CUDA-core kernel:
-// query rows, keys per step, CTAs an SM runs at once, and what an item and
-// the join of split results cost beside the steps, in steps (fitted: about
-// 1.5 us a step of the first kernel, 3 of the second).
+// query rows, keys per step, CTAs an SM runs at once, what an item costs
+// beside its steps and the join's launch, in steps (about 1.5 us of the
+// first kernel, 4 of the second), and the bytes of partial results that are
+// written and read in the time of a step.
 struct ItemShape {
     int rows, keys, resident;
-    double item_steps, join_steps;
+    double item_steps, join_steps, step_bytes;
 };
-constexpr ItemShape kTcShape{kTcRows, kTcKeys, 1, 3.0, 4.0};
-constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 1.0, 2.0};
-constexpr ItemShape kSimtFewShape{kSimtFewRows, kSimtKeys, 2, 1.0, 3.0};
+constexpr ItemShape kTcShape{kTcRows, kTcKeys, 1, 2.0, 3.0, 7.5e6};
+constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
+constexpr ItemShape kSimtFewShape{kSimtFewRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
+
+// A sequence of a call: its batch row, first packed row, queries, and the
+// longest and the mean length of its heads.
+struct AttendSeq {
+    int32_t brow, start, nq, n, mean;
+};
 
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
 // The candidates cut the longest sequence into 1 .. 64 parts; partial results
-// must fit the work buffer.
-template <class Seq>
-int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const Seq* sq, int nseq, int64_t total) {
+// must fit the work buffer.  Splitting pays where few rows see many keys:
+// five drafted tokens over eight 8K-32K caches take 122 us in three parts and
+// 316 us in one, 512 tokens over 16K 179 us in one part and 210 in seven (the
+// 238 MB of partial results cost more than even work gains).
+int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* sq, int nseq, int64_t total) {
+    static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
     const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = (int64_t)k.resident * c->sm_count;
     int64_t base_items = 0;
     for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows) * c->Hkv;
     if (base_items >= 4 * slots) return INT32_MAX;
-    const int64_t room = (int64_t)c->units * c->cap * c->G;   // floats of the work buffer
     double best = 0;
     int32_t best_chunk = INT32_MAX;
     int64_t last = 0;
-    for (int parts = 1; parts <= 64; ++parts) {
+    for (const int parts : kParts) {
         const int64_t ct = (maxsteps + parts - 1) / parts;   // steps per split
         if (ct == last || (parts > 1 && ct < 2)) continue;
         last = ct;
         const int64_t splits = (maxsteps + ct - 1) / ct;
-        if (splits > 1 && splits * total * c->Hq * (c->d + 2) > room) break;
+        const int64_t partial = splits * total * c->Hq * (c->d + 2);
+        if (splits > 1 && partial > c->attend_room) break;
         int64_t items = 0;
         double steps = 0, longest = 0;
         for (int i = 0; i < nseq; ++i) {
             const int64_t tiles = ((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows;
+            const double share = (double)sq[i].mean / sq[i].n;
             for (int64_t t = 0; t < tiles; ++t) {
                 const int64_t seen = sq[i].n - sq[i].nq + std::min<int64_t>(sq[i].nq, (t + 1) * k.rows / c->G);
                 const int64_t st = (seen + k.keys - 1) / k.keys;
                 items += (st + ct - 1) / ct * c->Hkv;
-                steps += (double)st * c->Hkv;
+                steps += share * st * c->Hkv;
                 longest = std::max(longest, (double)std::min(st, ct));
             }
         }
         double cost = std::max((steps + items * k.item_steps) / slots, longest + k.item_steps);
         if (items > slots) cost += 0.5 * longest;
-        if (splits > 1) cost += k.join_steps;
+        if (splits > 1) cost += k.join_steps + 8.0 * partial / k.step_bytes;
         if (parts == 1 || cost < best) {
             best = cost;
             best_chunk = splits > 1 ? (int32_t)(ct * k.keys) : INT32_MAX;
@@ -130,20 +141,21 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
     a.qscale = c->scale * 1.4426950408889634f;
     a.part_rows = total * c->Hq;
     // the sequences with queries, longest first: the work items start with the heaviest
-    struct Seq { int32_t brow, start, nq, n; };
-    std::vector<Seq> seqs;
+    std::vector<AttendSeq> seqs;
     for (int b = 0, row = 0; b < c->B; row += nq[b++])
         if (nq[b] > 0) {
             const int32_t* len = c->len.data() + u0 + b * c->Hkv;
-            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv)});
+            int64_t sum = 0;
+            for (int g = 0; g < c->Hkv; ++g) sum += len[g];
+            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv), (int32_t)(sum / c->Hkv)});
         }
-    std::stable_sort(seqs.begin(), seqs.end(), [](const Seq& x, const Seq& y) { return x.n > y.n; });
+    std::stable_sort(seqs.begin(), seqs.end(), [](const AttendSeq& x, const AttendSeq& y) { return x.n > y.n; });
     int64_t large = 0;   // work items of the CUDA-core kernel's larger shape
-    for (const Seq& x : seqs) large += (((int64_t)x.nq * c->G + kSimtRows - 1) / kSimtRows) * c->Hkv;
+    for (const AttendSeq& x : seqs) large += (((int64_t)x.nq * c->G + kSimtRows - 1) / kSimtRows) * c->Hkv;
     const ItemShape& shape = tc ? kTcShape : (large >= 2 * c->sm_count ? kSimtShape : kSimtFewShape);
     for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
-        const Seq* sq = seqs.data() + s0;
+        const AttendSeq* sq = seqs.data() + s0;
         a.chunk = attend_chunk(c, shape, sq, a.nseq, total);
         int64_t items = 0, split_tokens = 0, splits_max = 0;
         for (int i = 0; i < a.nseq; ++i) {
@@ -162,8 +174,8 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.item0[a.nseq] = a.items = (int32_t)items;
         a.comb0[a.nseq] = (int32_t)split_tokens;
         a.splits = (int32_t)splits_max;
-        a.part = c->d_logits;
-        a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
+        a.part = c->d_attend;
+        a.part_ml = c->d_attend + splits_max * a.part_rows * c->d;
         cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
                            : launch_attend_simt(a, c->d, shape.rows, (cudaStream_t)stream);
         c->launches += 1;
