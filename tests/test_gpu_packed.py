@@ -336,6 +336,69 @@ def test_attention_long_cache_few_rows_and_many(hk):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("bf16", 64, 8, 1), ("f32", 128, 4, 2), ("f32", 64, 8, 1)])
+@pytest.mark.parametrize("new,held,cut", [([3], [9000], None), ([40, 1, 0], [9000, 300, 50], None),
+                                          ([5, 70], [7000, 6000], [5000, 100]), ([33], [12000], [40, 9000])])
+def test_attention_split_keys(hk, dtype, d, hq, hkv, new, held, cut):
+    """Few rows over long keys, which several work items share: heads cut to
+    lengths of their own, among them some shorter than one part."""
+    gen = gen_of(sum(held) + hq)
+    cap = max(a + b for a, b in zip(new, held))
+    cache = make(hk, len(new), hq, hkv, d, dtype, cap, budgets=cut[:hkv] if cut else None)
+    for i, n in enumerate((held, new)):
+        t = sum(n)
+        cache.append_packed(rnd(gen, t, hkv, d, dtype=dtype), rnd(gen, t, hkv, d, dtype=dtype), n)
+        if i == 0:
+            cache.evict()
+    q = rnd(gen, sum(new), hq, d, dtype=dtype)
+    out = torch.empty_like(q)
+    launches = cache.kernel_launches()
+    cache.attend_packed(q, out, new)
+    # the parts and their join (one head cut to 40 tokens leaves nothing to split)
+    assert cache.kernel_launches() == launches + (2 if cache.lengths().max() > 1000 else 1)
+    cache.device_status()
+    check_attend(cache, q, out, new)
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("f32", 64, 4, 2)])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_non_finite_values_in_split_keys(hk, dtype, d, hq, hkv, value, monkeypatch):
+    """A non-finite V element among the new tokens of a split call."""
+    monkeypatch.setenv("HIKV_DEBUG", "1")
+    gen = gen_of(57)
+    held, n, bad = 6000, 20, 6009
+    k, v = rnd(gen, held + n, hkv, d, dtype=dtype), rnd(gen, held + n, hkv, d, dtype=dtype)
+    q = rnd(gen, n, hq, d, dtype=dtype)
+    v[bad, :, 5] = value
+    cache = make(hk, 1, hq, hkv, d, dtype, 6100)
+    cache.append_packed(k, v, [held + n])
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, [n])
+    head = make(hk, 1, hq, hkv, d, dtype, 6100)
+    m = bad - held
+    head.append_packed(k[:bad], v[:bad], [bad])
+    check_attend(head, q[:m], out[:m], [m])
+    assert not bool(torch.isfinite(out[m:, :, 5]).any())
+    assert bool(torch.isfinite(out[:, :, [i for i in range(d) if i != 5]]).all())
+    cache.device_status()
+
+
+def test_attention_with_an_unread_error_pending(hk):
+    """Another kernel's recorded time-out does not keep the queries from being answered."""
+    gen = gen_of(59)
+    cache = make(hk, 1, 8, 2)
+    x, q = rnd(gen, 100, 2, 128), rnd(gen, 100, 8, 128)
+    cache.append_packed(x, x, [100])
+    cache.selftest_timeout(1000)
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, [100])
+    check_attend(cache, q, out, [100])
+    with pytest.raises(hk.HikvError) as ei:
+        cache.device_status()
+    assert ei.value.status == hk.HIKV_ERR_TIMEOUT
+    cache.device_status()
+
+
 def test_attention_large_logits(hk):
     """Rows whose maximum keeps growing along the keys, and far negative ones."""
     gen = gen_of(43)
