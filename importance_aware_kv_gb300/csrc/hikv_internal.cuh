@@ -656,7 +656,7 @@ cudaError_t launch_append_packed(PackedAppendArgs& a, int dtype, int sm_count, c
 // sequence by sequence (longest first) and in a sequence from its last tile,
 // which sees most, to its first.  As the packed batch above, the sequences
 // come in kernel parameters.
-constexpr int kAttSeqs = 160;
+constexpr int kAttSeqs = 144;
 struct AttendArgs {
     View v;
     int32_t u0;             // unit of (the layer, batch row 0, KV head 0)
@@ -672,6 +672,7 @@ struct AttendArgs {
     int32_t brow[kAttSeqs];        // batch row
     int32_t start[kAttSeqs];       // first packed row
     int32_t nq[kAttSeqs];          // queries
+    int32_t len[kAttSeqs];         // tokens its units hold, -1: not all the same (read v.len)
     int32_t item0[kAttSeqs + 1];   // first work item
     int32_t comb0[kAttSeqs + 1];   // tokens of the sequences before it whose items are split
 };
@@ -686,6 +687,10 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
     return lo;
 }
 // `rows`: query rows of a work item, kSimtRows or, for calls with little work, kSimtFewRows
+// tokens of unit u, of sequence i of the call
+__device__ __forceinline__ int32_t unit_len(const AttendArgs& a, int32_t i, int32_t u) {
+    return a.len[i] >= 0 ? a.len[i] : a.v.len[u];
+}
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, int rows, cudaStream_t s);
 constexpr int kSimtRows = 64, kSimtFewRows = 32;
 constexpr int kSimtKeys = 64;   // keys per tile

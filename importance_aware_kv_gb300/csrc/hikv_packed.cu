@@ -60,9 +60,10 @@ constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
 constexpr ItemShape kSimtFewShape{kSimtFewRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
 
 // A sequence of a call: its batch row, first packed row, queries, and the
-// longest and the mean length of its heads.
+// longest and the mean length of its heads, and whether all are as long.
 struct AttendSeq {
     int32_t brow, start, nq, n, mean;
+    bool equal;
 };
 
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
@@ -146,8 +147,12 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         if (nq[b] > 0) {
             const int32_t* len = c->len.data() + u0 + b * c->Hkv;
             int64_t sum = 0;
-            for (int g = 0; g < c->Hkv; ++g) sum += len[g];
-            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv), (int32_t)(sum / c->Hkv)});
+            bool equal = true;
+            for (int g = 0; g < c->Hkv; ++g) {
+                sum += len[g];
+                equal &= len[g] == len[0];
+            }
+            seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv), (int32_t)(sum / c->Hkv), equal});
         }
     std::stable_sort(seqs.begin(), seqs.end(), [](const AttendSeq& x, const AttendSeq& y) { return x.n > y.n; });
     int64_t large = 0;   // work items of the CUDA-core kernel's larger shape
@@ -164,6 +169,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             a.brow[i] = sq[i].brow;
             a.start[i] = sq[i].start;
             a.nq[i] = sq[i].nq;
+            a.len[i] = sq[i].equal ? sq[i].n : -1;
             a.item0[i] = (int32_t)items;
             a.comb0[i] = (int32_t)split_tokens;
             items += tiles * splits * c->Hkv;

@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     if (tok >= a.comb0[a.nseq]) return;
     const int32_t i = prefix_find(a.comb0, a.nseq, tok);
     const int32_t j = tok - a.comb0[i];
-    const int32_t n = v.len[a.u0 + a.brow[i] * v.hkv + (h >> a.gshift)];
+    const int32_t n = unit_len(a, i, a.u0 + a.brow[i] * v.hkv + (h >> a.gshift));
     const int32_t lim = n - a.nq[i] + j;   // the row sees slots [0, lim]
     if (lim < 0 || n > v.cap) return;
     const int32_t ns = min(lim / a.chunk + 1, a.splits);

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_simt(const __grid_consta
     const int32_t rem = blockIdx.x - a.item0[i0], g = rem % v.hkv, split = rem / v.hkv % splits;
     const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * BM;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i0] * v.hkv + g;
-    const int32_t n = v.len[u];
+    const int32_t n = unit_len(a, i0, u);
     if (n < nq || n > v.cap) {
         if (tid == 0) atomicOr(v.err, DEVERR_STATE);
         return;

@@ -212,7 +212,7 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item&
     const int32_t rem = it - a.item0[i], x = rem / v.hkv;
     w.g = rem - x * v.hkv;
     w.u = a.u0 + a.brow[i] * v.hkv + w.g;
-    const int32_t n = v.len[w.u];
+    const int32_t n = unit_len(a, i, w.u);
     const int32_t splits = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
     const int32_t tile = splits > 1 ? x / splits : x;
     w.split = splits > 1 ? x - tile * splits : -1;
