@@ -19,7 +19,7 @@
 
 #include "../../include/hikv.h"
 #include "hikv_cache.cuh"
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 size_t window_smem_bytes(int d, int nqv);

@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "hikv_cache.cuh"
+#include "hikv_packed.cuh"
 
 using namespace hikv;
 

@@ -6,7 +6,7 @@
 // the unit's next free ones (the cache stays densely packed; eviction
 // compacts), pages come from the shared free stack (blog sec. 5.1: paged KV
 // blocks).
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 namespace {

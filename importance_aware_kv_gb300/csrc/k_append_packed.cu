@@ -17,7 +17,7 @@
 #include <algorithm>
 
 #include "../../include/hikv.h"
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 namespace {

@@ -1,6 +1,6 @@
 // The join of attention results whose keys were split over work items.
 #include "../../include/hikv.h"
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 namespace {

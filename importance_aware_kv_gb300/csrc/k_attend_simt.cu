@@ -17,7 +17,7 @@
 // 46.6 TFLOP/s); two CTAs share an SM, for which P lies over K at d = 128.
 // K and V come by asynchronous copies, at d = 64 a tile ahead.  With few rows
 // the keys are split over CTAs (chunk) and the parts joined.
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 namespace {

@@ -32,7 +32,7 @@
 //
 // Probabilities enter the product with V as bf16 (relative error 2^-8 each,
 // averaged over the keys); the sums l are of the fp32 values.
-#include "hikv_internal.cuh"
+#include "hikv_packed.cuh"
 
 namespace hikv {
 namespace {
