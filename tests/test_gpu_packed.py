@@ -298,6 +298,32 @@ def test_attention_strided_rows(hk):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layers_of_their_own(hk, dtype):
+    """Three layers at lengths of their own, k rotated without a q, in a cache
+    whose decode steps are element-level: attention is exact all the same."""
+    gen = gen_of(25)
+    cache = make(hk, 2, 4, 2, 64, dtype, 300, layers=3, element_budget=16)
+    cos, sin = tables(300, 64)
+    lens = [[100, 3], [1, 250], [64, 64]]
+    rows = []
+    for layer, n in enumerate(lens):
+        k, v = rnd(gen, sum(n), 2, 64, dtype=dtype), rnd(gen, sum(n), 2, 64, dtype=dtype)
+        cache.append_packed(k, v, np.array(n), layer=layer, rope=hk.Rope(cos, sin))
+        rows.append(k)
+    assert cache.lengths().tolist() == [x for n in lens for m in n for x in (m, m)]
+    for layer in (2, 0, 1):
+        n = lens[layer]
+        q = rnd(gen, sum(n), 4, 64, dtype=dtype)
+        out = torch.empty_like(q)
+        cache.attend_packed(q, out, torch.tensor(n), layer=layer)
+        check_attend(cache, q, out, n, layer)
+        y, mag = rotated(rows[layer], torch.cat([torch.arange(m, device=DEV) for m in n]), cos, sin, False)
+        for g in range(2):
+            close_rot(slots(cache, 4 * layer + g)[0], y[:n[0], g], mag[:n[0], g], dtype)
+    cache.device_status()
+
+
 @pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("bf16", 64, 16, 2), ("f32", 64, 4, 2)])
 @pytest.mark.parametrize("sizes", [[1] * 9, [64, 64, 44], [130, 1, 41]])
 def test_chunks_of_a_prompt_give_the_whole(hk, dtype, d, hq, hkv, sizes):
