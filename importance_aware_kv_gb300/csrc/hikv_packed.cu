@@ -47,18 +47,16 @@ int64_t packed_total(const hikv_cache* c, const int32_t* ntok) {
     return total <= INT32_MAX ? total : -1;
 }
 
-// The shape of the work items of the tensor-core and of the CUDA-core kernel:
-// query rows, keys per step, CTAs an SM runs at once, what an item costs
-// beside its steps and the join's launch, in steps (about 1.5 us of the
-// first kernel, 4 of the second), and the bytes of partial results that are
-// written and read in the time of a step.
+// The shape of the work items of the bf16 and of the fp32 kernel: query rows,
+// keys per step, what an item costs beside its steps and the join's launch,
+// in steps (about 1.5 us of the first kernel, 3 of the second), and the bytes
+// of partial results that are written and read in the time of a step.
 struct ItemShape {
-    int rows, keys, resident;
+    int rows, keys;
     double item_steps, join_steps, step_bytes;
 };
-constexpr ItemShape kTcShape{kTcRows, kTcKeys, 1, 2.0, 3.0, 7.5e6};
-constexpr ItemShape kSimtShape{kSimtRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
-constexpr ItemShape kSimtFewShape{kSimtFewRows, kSimtKeys, 2, 0.4, 1.0, 20e6};
+constexpr ItemShape kTcShape{kTcRows, kTcKeys, 2.0, 3.0, 7.5e6};
+constexpr ItemShape kF32Shape{kF32Rows, kF32Keys, 1.5, 1.5, 15e6};
 
 // A sequence of a call: its batch row, first packed row, queries, and the
 // longest and the mean length of its heads, and whether all are as long.
@@ -75,7 +73,7 @@ struct AttendSeq {
 // 238 MB of partial results cost more than even work gains).
 int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* sq, int nseq, int64_t total) {
     static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
-    const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = (int64_t)k.resident * c->sm_count;
+    const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = c->sm_count;
     int64_t base_items = 0;
     for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows) * c->Hkv;
     if (base_items >= 4 * slots) return INT32_MAX;
@@ -119,9 +117,9 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
     DeviceGuard guard(c->device);
     if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
     pdl_forget(c);
-    const bool tc = c->dtype == HIKV_BF16;
+    const bool bf16 = c->dtype == HIKV_BF16;
     CUtensorMap qmap;
-    if (tc) {
+    if (bf16) {
         // q as [tokens][heads][d], boxes of 128 query rows x 128 bytes
         cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->Hq, (cuuint64_t)total};
         cuuint64_t strides[2] = {(cuuint64_t)(c->Hq > 1 ? q->head_stride : c->d) * 2,
@@ -156,9 +154,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             seqs.push_back({b, row, nq[b], *std::max_element(len, len + c->Hkv), (int32_t)(sum / c->Hkv), equal});
         }
     std::stable_sort(seqs.begin(), seqs.end(), [](const AttendSeq& x, const AttendSeq& y) { return x.n > y.n; });
-    int64_t large = 0;   // work items of the CUDA-core kernel's larger shape
-    for (const AttendSeq& x : seqs) large += (((int64_t)x.nq * c->G + kSimtRows - 1) / kSimtRows) * c->Hkv;
-    const ItemShape& shape = tc ? kTcShape : (large >= 2 * c->sm_count ? kSimtShape : kSimtFewShape);
+    const ItemShape& shape = bf16 ? kTcShape : kF32Shape;
     for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const AttendSeq* sq = seqs.data() + s0;
@@ -183,8 +179,8 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.splits = (int32_t)splits_max;
         a.part = c->d_attend;
         a.part_ml = c->d_attend + splits_max * a.part_rows * c->d;
-        cudaError_t e = tc ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
-                           : launch_attend_simt(a, c->d, shape.rows, (cudaStream_t)stream);
+        cudaError_t e = bf16 ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
+                             : launch_attend_f32(a, c->d, (cudaStream_t)stream);
         c->launches += 1;
         if (e == cudaSuccess && split_tokens > 0) {
             e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);

@@ -156,18 +156,15 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
     }
     return lo;
 }
-// `rows`: query rows of a work item, kSimtRows or, for calls with little work, kSimtFewRows
 // tokens of unit u, of sequence i of the call
 __device__ __forceinline__ int32_t unit_len(const AttendArgs& a, int32_t i, int32_t u) {
     return a.len[i] >= 0 ? a.len[i] : a.v.len[u];
 }
-cudaError_t launch_attend_simt(const AttendArgs& a, int d, int rows, cudaStream_t s);
-constexpr int kSimtRows = 64, kSimtFewRows = 32;
-constexpr int kSimtKeys = 64;   // keys per tile
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
                              cudaStream_t s);
-constexpr int kTcRows = 256;    // of the tensor-core kernel
-constexpr int kTcKeys = 128;    // keys per tile
+constexpr int kTcRows = 256, kTcKeys = 128;    // query rows of a work item of the bf16 kernel, keys per tile
+cudaError_t launch_attend_f32(const AttendArgs& a, int d, cudaStream_t s);
+constexpr int kF32Rows = 128, kF32Keys = 64;   // of the fp32 kernel
 cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s);
 
 constexpr int kDropMax = 512;

@@ -9,7 +9,8 @@ fp32, relative to the value; u = 2^-24):
         h |y| + 3 u (|a c| + |b s|);
   * attention: a logit is a sum of d products in fp32, off by at most
     2 d u scale sum |q k| (twice the bound of a rounded sum, since a matrix
-    unit may truncate where it aligns); an error e in every logit moves the
+    unit may truncate where it aligns; fp32 operands in three bf16 parts lose 3 u
+    of each product, far inside that); an error e in every logit moves the
     output by at most (exp(2 e) - 1) sum p |v|; the exponential by 4 u of its
     value; sums of n terms by 2 n u; probabilities rounded to the cache dtype
     in front of the product with V by h each; then the output's rounding:
