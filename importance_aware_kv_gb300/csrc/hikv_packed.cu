@@ -136,6 +136,9 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
     a.v = c->v;
     a.u0 = u0;
     while ((1 << a.gshift) < c->G) ++a.gshift;
+    a.hkv_shift = 0;
+    while ((1 << a.hkv_shift) < c->Hkv) ++a.hkv_shift;
+    if ((1 << a.hkv_shift) != c->Hkv) a.hkv_shift = -1;
     a.q = rows_arg(c, q);
     a.out = rows_arg(c, out);
     a.qscale = c->scale * 1.4426950408889634f;
@@ -167,6 +170,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             a.start[i] = sq[i].start;
             a.nq[i] = sq[i].nq;
             a.len[i] = sq[i].equal ? sq[i].n : -1;
+            a.parts[i] = (int32_t)splits;
             a.item0[i] = (int32_t)items;
             a.comb0[i] = (int32_t)split_tokens;
             items += tiles * splits * c->Hkv;

@@ -126,7 +126,7 @@ cudaError_t launch_append_packed(PackedAppendArgs& a, int dtype, int sm_count, c
 // sequence by sequence (longest first) and in a sequence from its last tile,
 // which sees most, to its first.  As the packed batch above, the sequences
 // come in kernel parameters.
-constexpr int kAttSeqs = 144;
+constexpr int kAttSeqs = 128;
 struct AttendArgs {
     View v;
     int32_t u0;             // unit of (the layer, batch row 0, KV head 0)
@@ -138,11 +138,13 @@ struct AttendArgs {
     float* part_ml;         // ... [splits][part_rows][2] maxima and sums
     int64_t part_rows;      // rows (t, h) of the packed batch
     int32_t splits;         // the most parts a sequence's keys are split into
+    int32_t hkv_shift;      // log2 of the KV heads, -1: no power of two
     int32_t nseq, items;
     int32_t brow[kAttSeqs];        // batch row
     int32_t start[kAttSeqs];       // first packed row
     int32_t nq[kAttSeqs];          // queries
     int32_t len[kAttSeqs];         // tokens its units hold, -1: not all the same (read v.len)
+    int32_t parts[kAttSeqs];       // parts its keys are split into
     int32_t item0[kAttSeqs + 1];   // first work item
     int32_t comb0[kAttSeqs + 1];   // tokens of the sequences before it whose items are split
 };

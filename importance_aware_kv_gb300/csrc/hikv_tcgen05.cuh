@@ -67,6 +67,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::I8(r, 0), "r"(addr)
                  : "memory");
 }
+// one column, complete
+__device__ __forceinline__ void tmem_ld1(uint32_t& r, uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "

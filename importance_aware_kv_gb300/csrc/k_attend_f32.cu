@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     // the work item: rows [r0, r0 + kRows) of (sequence i, KV head g), keys [lo, end)
     const int32_t i = prefix_find(a.item0, a.nseq, blockIdx.x);
     const int32_t nq = a.nq[i], first = a.start[i], rows = nq << a.gshift, tiles = ceil_div(rows, kRows);
-    const int32_t splits = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
+    const int32_t splits = a.parts[i];
     const int32_t rem = blockIdx.x - a.item0[i], g = rem % v.hkv, split = rem / v.hkv % splits;
     const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * kRows;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i] * v.hkv + g;

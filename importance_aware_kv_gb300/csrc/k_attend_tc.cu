@@ -95,11 +95,11 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item&
     w.some = 1;
     w.rows = nq << a.gshift;
     const int32_t tiles = (w.rows + kRows - 1) / kRows;
-    const int32_t rem = it - a.item0[i], x = rem / v.hkv;
+    const int32_t rem = it - a.item0[i], x = a.hkv_shift >= 0 ? rem >> a.hkv_shift : rem / v.hkv;
     w.g = rem - x * v.hkv;
     w.u = a.u0 + a.brow[i] * v.hkv + w.g;
     const int32_t n = unit_len(a, i, w.u);
-    const int32_t splits = (a.item0[i + 1] - a.item0[i]) / (tiles * v.hkv);
+    const int32_t splits = a.parts[i];
     const int32_t tile = splits > 1 ? x / splits : x;
     w.split = splits > 1 ? x - tile * splits : -1;
     w.r0 = (tiles - 1 - tile) * kRows;
@@ -237,14 +237,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // (a wait of this kernel gave up: start nothing more, each item would wait as long)
+    uint32_t err0 = 0, err1 = 0;
+    if (warp == 8) {
+        err0 = reinterpret_cast<const volatile uint32_t*>(v.err)[0];
+        err1 = reinterpret_cast<const volatile uint32_t*>(v.err)[1];
+    }
     griddep_wait();   // what the kernel before writes is there: lengths, pages, q
     Item w0;
     if (warp == 8) {
-        // (a wait of this kernel gave up: start nothing more, each item would wait as long)
-        const volatile uint32_t* err = v.err;
-        const bool bad = (err[0] & DEVERR_TIMEOUT) != 0 && err[1] == kWaitAttend;
         if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
-        w0.some = !bad;
+        w0.some = !((err0 & DEVERR_TIMEOUT) != 0 && err1 == kWaitAttend);
     }
     tc_fence_before();
     __syncthreads();
@@ -341,7 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!warp_wait(&o_full[tile], ophase, v.err, 0x200)) { ok = false; break; }
                 ophase ^= 1;
                 tc_fence_after();
-                const bool over_here = misc[2] == items.n;
+                if (misc[2] == items.n) {
+                    // (rare) non-finite values of the edge tiles, for the rows that see them
+#pragma unroll 1
+                    for (int j = 0; j < D; ++j) {
+                        uint32_t o;
+                        tmem_ld1(o, to + j);
+                        float x = __uint_as_float(o);
+                        if (over[j] <= lim) x += INFINITY;
+                        if (over[D + j] <= lim) x -= INFINITY;
+                        if (over[2 * D + j] <= lim) x = __int_as_float(0x7FC00000);
+                        tmem_st1(to + j, __float_as_uint(x));
+                    }
+                    tmem_wait_st();
+                }
                 const float inv = w.split < 0 ? 1.0f / l : 1.f;
                 // lane i of each four ends up with the i-th 32 bytes of four rows' 128
                 const int32_t row4 = row & ~3;
@@ -355,27 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 a.part + ((int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h) * D)) +
                              32 * (lane & 3);
                 }
-#pragma unroll
-                for (int j = 0; j < D; j += 64) {
-                    uint32_t o[64];
-                    tmem_ld32(o, to + j);
-                    tmem_ld32(o + 32, to + j + 32);
-                    tmem_wait_ld();
-                    held(o);
-                    held(o + 32);
-                    if (over_here) {
-                        // non-finite values of the edge tiles, for the rows that see them
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) {
-                            float x = __uint_as_float(o[i]);
-                            if (over[j + i] <= lim) x += INFINITY;
-                            if (over[D + j + i] <= lim) x -= INFINITY;
-                            if (over[2 * D + j + i] <= lim) x = __int_as_float(0x7FC00000);
-                            o[i] = __float_as_uint(x);
-                        }
-                    }
-                    uint32_t x[4][8];
-                    if (w.split < 0) {
+                // (not unrolled: an item runs this once, from a cold instruction cache)
+                if (w.split < 0) {
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 64) {
+                        uint32_t o[64], x[4][8];
+                        tmem_ld32(o, to + j);
+                        tmem_ld32(o + 32, to + j + 32);
+                        tmem_wait_ld();
+                        held(o);
+                        held(o + 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             x[i / 8][i % 8] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
@@ -383,16 +388,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (row4 + i < w.rows) store32(dst[i] + 2 * j, x[i], wide);
-                    } else {
+                    }
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 32) {
+                        uint32_t x[4][8];
+                        tmem_ld32(&x[0][0], to + j);
+                        tmem_wait_ld();
+                        held(&x[0][0]);
+                        quad_transpose(x, lane);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i / 8][i % 8] = o[32 * k + i];
-                            quad_transpose(x, lane);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (row4 + i < w.rows) store32(dst[i] + 4 * j + 128 * k, x[i], true);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (row4 + i < w.rows) store32(dst[i] + 4 * j, x[i], true);
                     }
                 }
                 if (w.split >= 0 && row < w.rows) {
@@ -443,25 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         w = w0;
-        if (w.some) {
+        if (w.some && w.ntiles == 0) {
             ask();
-            if (w.ntiles == 0) next_item(w);
+            next_item(w);
         }
         uint32_t loaded = 0;
         if (ok) hand_out(w);
         while (ok && w.some) {
-            if (asked == read) ask();
-            if (loaded > 0) ok = warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x300);
-            if (!ok) break;
-            ++loaded;
-            if (lane == 0) {
-                const int tiles = w.r0 + 128 < w.rows ? 2 : 1;
-                mbar_arrive_expect_tx(q_full, tiles * C::TILE);
-                for (int t = 0; t < tiles; ++t)
-                    for (int hf = 0; hf < C::HALVES; ++hf)
-                        tma_load_3d(sm + C::OFF_Q + t * C::TILE + hf * C::BLOCK, &qmap, 64 * hf, w.g << a.gshift,
-                                    w.first + ((w.r0 + 128 * t) >> a.gshift), q_full);
-            }
             Item next;
             const int32_t fills = 2 * w.ntiles, when = min(4, fills);
             for (int32_t x = 0; ok && x <= fills; ++x) {
@@ -470,6 +465,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ok) hand_out(next);
                 }
                 if (x == fills || !ok) break;
+                if (x == 1) {   // the first keys wait for nothing
+                    if (loaded > 0) ok = warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x300);
+                    if (!ok) break;
+                    ++loaded;
+                    const int tiles = w.r0 + 128 < w.rows ? 2 : 1;
+                    if (lane == 0) mbar_arrive_expect_tx(q_full, tiles * C::TILE);
+                    __syncwarp();
+                    if (lane < tiles * C::HALVES) {
+                        const int t = lane / C::HALVES, hf = lane % C::HALVES;
+                        tma_load_3d(sm + C::OFF_Q + t * C::TILE + hf * C::BLOCK, &qmap, 64 * hf, w.g << a.gshift,
+                                    w.first + ((w.r0 + 128 * t) >> a.gshift), q_full);
+                    }
+                    if (asked == read) ask();
+                }
                 const int st = fill % C::STAGES;
                 const uint32_t use = fill / C::STAGES;
                 if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, v.err, 0x400 + st)) { ok = false; break; }
