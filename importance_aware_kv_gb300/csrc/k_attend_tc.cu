@@ -32,6 +32,15 @@
 //
 // Probabilities enter the product with V as bf16 (relative error 2^-8 each,
 // averaged over the keys); the sums l are of the fp32 values.
+//
+// Measured: 16K tokens with 64/8 heads, d = 128, 2.63 ms, 1.67 PFLOP/s; 8K with
+// 32/8 345 us, 1.59; five tokens over eight 8K-32K caches 119 us, 6.1 TB/s of
+// keys and values.  What bounds a long prompt: a row tile's step takes about
+// 2,450 cycles (softmax 770 to the first half of P, waking the issuing thread
+// 400, the products 1,024, their latency 340) where the products of both
+// tiles need 2,048, and the chip runs at its power limit.  256 rows an item
+// because each key tile is then read from L2 once for two row tiles (64 KB a
+// step and SM; one row tile would double that to more than L2 delivers).
 #include "hikv_tcgen05.cuh"
 
 namespace hikv {

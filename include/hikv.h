@@ -354,8 +354,11 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
  * (which may have been cut, to another length for every head), the tokens of
  * a speculative verification, or one token; append them first.  Neither
  * importance nor any other state changes (hikv_score_window and
- * hikv_decode_step score).  Softmax statistics and sums are fp32.  A K or V
- * row that a query does not see does not touch its output, whatever it holds.
+ * hikv_decode_step score).  Softmax statistics and sums are fp32; bf16 caches
+ * round the probabilities to bf16 for the product with V, fp32 caches form
+ * every product to 2^-22 of it.  A K or V row that a query does not see does
+ * not touch its output, whatever it holds.  (fp32: a non-finite element of
+ * q, or of a k that is seen, makes the row NaN.)
  * out: [sum nq][Hq] rows, written; must not overlap q.  Always exact
  * attention, with an element_budget too.  May be captured as
  * hikv_append_packed.
