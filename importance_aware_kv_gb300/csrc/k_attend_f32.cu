@@ -12,17 +12,20 @@
 //
 // A work item is 128 query rows (row = token * G + head) of one KV head, its
 // keys in tiles of 64:
-//   warps 0-3   softmax, one thread a row: S of a tile from tensor memory, the three
-//               parts of P back, the row's output sums in registers
-//   warps 4-11  read Q, K (4-7) and V (8-11) from global memory and write their parts
-//               to shared memory, swizzled as the products want them
+//   warps 0-3   softmax, one thread a row: the parts of its query into tensor
+//               memory, S of a tile from there, the parts of P back, the row's
+//               output sums in registers
+//   warps 4-11  read K (4-7) and V (8-11) from global memory and write their parts to
+//               shared memory, swizzled as the products want them, two tiles each
 //   warp 12     one thread issues the products; S of the next tile forms under the
-//               softmax of this one (two places in tensor memory)
-// Six products bound it: 2,304 cycles for S (64-column tiles read their
-// operands at 128 bytes a cycle) and 1,536 for P V per 128 x 64 tile; with the
-// splitting beside them a tile takes about 6,000 (4096 tokens with 32/8 heads, d =
-// 128: 695 us, 198 TFLOP/s of fp32 work; the same on the CUDA cores, 4 x 4
-// tiles in registers, 2,947 us and 46.7).
+//               softmax of this one, whose S is in registers by then
+// Queries in tensor memory leave shared memory to two tiles of keys and values.
+// What bounds it: the six products.  A 128 x 64 x 16 product takes 73 cycles, as
+// long as one of 128 columns would (its rows' operand, 4 KB, comes at 64 bytes a
+// cycle), so a 128 x 64 tile's S takes 3,500 cycles and its P V 1,536 of the
+// 5,800 a step; 128 keys a tile would need 544 columns of tensor memory.
+// 4096 tokens with 32/8 heads, d = 128: 697 us, 197 TFLOP/s of fp32 work (the same
+// on the CUDA cores, 4 x 4 tiles in registers: 2,947 us, 46.7).
 //
 // Non-finite V elements do not go through the products (0 x inf): they are
 // noted with their slots and added to the rows that see them.  A non-finite
@@ -40,19 +43,18 @@ constexpr int kRegsSoftmax = 224, kRegsOther = 96;
 template <int D>
 struct F3 {
     static constexpr int HALVES = D / 64;
-    static constexpr int QBLOCK = kRows * 128, KBLOCK = kKeys * 128;   // 64 columns of a part
-    static constexpr int QPART = HALVES * QBLOCK, KPART = HALVES * KBLOCK;
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = 3 * QPART;
-    static constexpr int OFF_V = OFF_K + 3 * KPART;
-    // barriers: q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_full, o_full, drained
-    static constexpr int OFF_BAR = OFF_V + 3 * KPART;
-    static constexpr int OFF_MISC = OFF_BAR + 10 * 8;     // tensor memory address, non-finite values noted
+    static constexpr int KBLOCK = kKeys * 128;            // 64 columns of a part
+    static constexpr int KPART = HALVES * KBLOCK, TILE = 3 * KPART;
+    static constexpr int OFF_K = 0;                       // two tiles
+    static constexpr int OFF_V = 2 * TILE;
+    // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_read, p_full, o_full, drained
+    static constexpr int OFF_BAR = 4 * TILE;
+    static constexpr int OFF_MISC = OFF_BAR + 14 * 8;     // tensor memory address, non-finite values noted
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
-// columns of tensor memory
-constexpr int kTmS = 0, kTmP = 128, kTmO = 256;
+// columns of tensor memory: three parts of Q, S, three parts of P, O
+constexpr int kTmQ = 0, kTmS = 192, kTmP = 256, kTmO = 352;
 
 // magnitudes that round to a bf16 infinity, and NaN
 __device__ __forceinline__ bool rounds_to_inf(float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F7F8000u; }
@@ -96,13 +98,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     using C = F3<D>;
     extern __shared__ __align__(128) uint8_t raw[];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-    uint64_t* k_full = q_full + 1;
-    uint64_t* k_empty = k_full + 1;
-    uint64_t* v_full = k_empty + 1;
-    uint64_t* v_empty = v_full + 1;
-    uint64_t* s_full = v_empty + 1;
-    uint64_t* p_full = s_full + 2;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+    uint64_t* k_empty = k_full + 2;
+    uint64_t* v_full = k_empty + 2;
+    uint64_t* v_empty = v_full + 2;
+    uint64_t* q_full = v_empty + 2;
+    uint64_t* s_full = q_full + 1;
+    uint64_t* s_read = s_full + 1;
+    uint64_t* p_full = s_read + 1;
     uint64_t* o_full = p_full + 1;
     uint64_t* drained = o_full + 1;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
@@ -111,13 +114,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, kConvert / 32);
-        mbar_init(k_full, kConvert / 64);
-        mbar_init(k_empty, 1);
-        mbar_init(v_full, kConvert / 64);
-        mbar_init(v_empty, 1);
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], kConvert / 64);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], kConvert / 64);
+            mbar_init(&v_empty[i], 1);
+        }
+        mbar_init(q_full, 4);
+        mbar_init(s_full, 1);
+        mbar_init(s_read, 4);
         mbar_init(p_full, 4);
         mbar_init(o_full, 1);
         mbar_init(drained, 1);
@@ -167,11 +172,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
         const int32_t lim = seen0 + (min(row, rows - 1) >> a.gshift);                     // sees slots [0, lim]
         const int32_t lim_w = seen0 + (min(r0 + 32 * warp, rows - 1) >> a.gshift);        // the warp's first row
         const float c = a.qscale;
+        bool ok = run;
+        {
+            // this row's query in parts, 16 elements (8 columns of each part) at a time
+            const int32_t tok = first + (row >> a.gshift), h = (g << a.gshift) + (row & ((1 << a.gshift) - 1));
+            const float4* src = reinterpret_cast<const float4*>(a.q.row(tok, h));
+#pragma unroll 2
+            for (int j = 0; j < D / 16; ++j) {
+                float x[16] = {};
+                if (row < rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(x + 4 * k) = src[4 * j + k];
+                    mark_nan(x);
+                    mark_nan(x + 8);
+                }
+                uint32_t hi[8], mi[8], lw[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) three_parts(make_float2(x[2 * k], x[2 * k + 1]), hi[k], mi[k], lw[k]);
+                const uint32_t tq = tmem + base_lane + kTmQ + 8 * j;
+                tmem_st8(tq, hi);
+                tmem_st8(tq + D / 2, mi);
+                tmem_st8(tq + D, lw);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
         float m = -INFINITY, l = 0.f;
         float2 acc[D / 2];
 #pragma unroll
         for (int j = 0; j < D / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-        bool ok = run;
         // add the tile's P V
         auto add = [&](uint32_t parity) {
             ok = warp_wait(o_full, parity, v.err, 0x800);
@@ -189,15 +220,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             }
         };
         for (int32_t t = 0; ok && t < nt; ++t) {
-            ok = warp_wait(&s_full[t & 1], (t >> 1) & 1, v.err, 0x801);
+            ok = warp_wait(s_full, t & 1, v.err, 0x801);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[64];
-            tmem_ld32(s, tmem + base_lane + kTmS + 64 * (t & 1));
-            tmem_ld32(s + 32, tmem + base_lane + kTmS + 64 * (t & 1) + 32);
+            tmem_ld32(s, tmem + base_lane + kTmS);
+            tmem_ld32(s + 32, tmem + base_lane + kTmS + 32);
             tmem_wait_ld();
             held(s);
             held(s + 32);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_read);   // the next tile's S may form
             const int32_t s0 = lo + t * kKeys;
             if (s0 + kKeys - 1 > lim_w || s0 + kKeys > end) {
                 const int32_t left = min(lim, end - 1) - s0;   // columns [0, left] are seen
@@ -301,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp < 12) {
-            // ---------------- parts of Q, K and V ----------------
+            // ---------------- parts of K and V ----------------
             constexpr int CHUNKS = D / 8;   // groups of eight elements of a row
             // a row's group of eight within a part: 128-byte rows of 64 columns, 16-byte pieces swizzled by the row
             auto place = [&](int chunk, int r, int block) {
@@ -312,27 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar);
             };
-            if (run) {
-                const int ct = threadIdx.x - 128, chunk = ct % CHUNKS;
-                for (int r = ct / CHUNKS; r < kRows; r += kConvert / CHUNKS) {
-                    float x[8] = {};
-                    if (r0 + r < rows) {
-                        const int32_t tok = first + ((r0 + r) >> a.gshift);
-                        const int32_t h = (g << a.gshift) + ((r0 + r) & ((1 << a.gshift) - 1));
-                        const float4* src = reinterpret_cast<const float4*>(a.q.row(tok, h)) + 2 * chunk;
-                        *reinterpret_cast<float4*>(x) = src[0];
-                        *reinterpret_cast<float4*>(x + 4) = src[1];
-                    }
-                    put_parts(sm + C::OFF_Q + place(chunk, r, C::QBLOCK), C::QPART, x, mark_nan);
-                }
-                done(q_full);
-            }
             // warps 4-7 take the keys, 8-11 the values: a tile's rows wait in
             // registers while the products of the tile before run
             const bool is_v = warp >= 8;
             constexpr int STEP = kConvert / 2 / CHUNKS, PER = kKeys / STEP;   // rows a pass, rows of a thread
             const int ct = (threadIdx.x - 128) % (kConvert / 2), chunk = ct % CHUNKS, row_t = ct / CHUNKS;
-            uint8_t* tile = sm + (is_v ? C::OFF_V : C::OFF_K);
+            uint8_t* tiles0 = sm + (is_v ? C::OFF_V : C::OFF_K);
             float x[PER][8];
             auto load = [&](int32_t s0) {
 #pragma unroll
@@ -348,8 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             if (run) load(lo);
             for (int32_t t = 0; ok && t < nt; ++t) {
                 const int32_t s0 = lo + t * kKeys;
-                if (t > 0) ok = warp_wait(is_v ? v_empty : k_empty, (t - 1) & 1, v.err, 0x802 + is_v);
+                if (t > 1) ok = warp_wait((is_v ? v_empty : k_empty) + (t & 1), ((t - 2) >> 1) & 1, v.err, 0x802 + is_v);
                 if (!ok) break;
+                uint8_t* tile = tiles0 + (t & 1) * C::TILE;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const int r = row_t + j * STEP;
@@ -367,15 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                     };
                     put_parts(tile + place(chunk, r, C::KBLOCK), C::KPART, x[j], mend);
                 }
-                done(is_v ? v_full : k_full);
+                done((is_v ? v_full : k_full) + (t & 1));
                 if (t + 1 < nt) load(s0 + kKeys);
             }
         } else if (warp == 12) {
             // ---------------- products ----------------
             if (elect_one()) {
                 constexpr uint32_t id_qk = idesc_of(128, kKeys, false), id_pv = idesc_of(128, D, true);
-                const uint64_t dq = sdesc(smem_u32(sm + C::OFF_Q), 16, 1024), dk = sdesc(smem_u32(sm + C::OFF_K), 16, 1024);
-                const uint64_t dv = sdesc(smem_u32(sm + C::OFF_V), C::KBLOCK, 1024);
+                const uint64_t dk = sdesc(smem_u32(sm + C::OFF_K), 16, 1024), dv = sdesc(smem_u32(sm + C::OFF_V), C::KBLOCK, 1024);
                 // the parts of the two operands, smallest products first (0: h, 1: m, 2: l)
                 constexpr int PA[6] = {1, 0, 2, 0, 1, 0}, PB[6] = {1, 2, 0, 1, 0, 0};
                 bool ok = run;
@@ -383,24 +402,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                     ok = ok && mbar_wait_bounded(bar, parity, v.err, kWaitAttend, index);
                 };
                 auto qk = [&](int32_t t) {   // S of tile t
-                    wait(k_full, t & 1, 0x804);
+                    const uint64_t b = dk + (t & 1) * (C::TILE >> 4);
+                    wait(&k_full[t & 1], (t >> 1) & 1, 0x804);
+                    if (t > 0) wait(s_read, (t - 1) & 1, 0x809);
                     if (!ok) return;
                     tc_fence_after();
 #pragma unroll
                     for (int p = 0; p < 6; ++p)
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_ss(tmem + kTmS + 64 * (t & 1),
-                                   dq + ((PA[p] * C::QPART + (k / 4) * C::QBLOCK + (k % 4) * 32) >> 4),
-                                   dk + ((PB[p] * C::KPART + (k / 4) * C::KBLOCK + (k % 4) * 32) >> 4), id_qk, p + k > 0);
-                    mma_commit(&s_full[t & 1]);
-                    mma_commit(k_empty);
+                            mma_ts(tmem + kTmS, tmem + kTmQ + PA[p] * (D / 2) + 8 * k,
+                                   b + ((PB[p] * C::KPART + (k / 4) * C::KBLOCK + (k % 4) * 32) >> 4), id_qk, p + k > 0);
+                    mma_commit(s_full);
+                    mma_commit(&k_empty[t & 1]);
                 };
                 wait(q_full, 0, 0x805);
                 if (ok) qk(0);
                 for (int32_t t = 0; ok && t < nt; ++t) {
                     if (t + 1 < nt) qk(t + 1);
-                    wait(v_full, t & 1, 0x806);
+                    const uint64_t b = dv + (t & 1) * (C::TILE >> 4);
+                    wait(&v_full[t & 1], (t >> 1) & 1, 0x806);
                     wait(p_full, t & 1, 0x807);
                     if (!ok) break;
                     tc_fence_after();
@@ -408,10 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                     for (int p = 0; p < 6; ++p)
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
-                            mma_ts(tmem + kTmO, tmem + kTmP + 32 * PA[p] + 8 * k,
-                                   dv + ((PB[p] * C::KPART + k * 2048) >> 4), id_pv, p + k > 0);
+                            mma_ts(tmem + kTmO, tmem + kTmP + 32 * PA[p] + 8 * k, b + ((PB[p] * C::KPART + k * 2048) >> 4), id_pv,
+                                   p + k > 0);
                     mma_commit(o_full);
-                    mma_commit(v_empty);
+                    mma_commit(&v_empty[t & 1]);
                 }
                 // nothing is in flight when the CTA ends, after a wait that gave up neither
                 mma_commit(drained);
