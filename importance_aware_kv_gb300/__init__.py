@@ -192,6 +192,7 @@ class Rope:
         self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
         self.device_index = cos.device.index
         self.c = hikv_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+        self.ref = ctypes.byref(self.c)
 
 
 class _DeviceArray:
@@ -347,6 +348,8 @@ class Cache:
         import torch
         self.device_index = torch.cuda.current_device()
         self._torch_dtype = self._dtype()
+        self._row_args = [hikv_rows() for _ in range(4)]   # k, v, q, q_out / out of a packed call
+        self._row_refs = [ctypes.byref(r) for r in self._row_args]
 
     def close(self):
         if getattr(self, "h", None) is not None and self.h.value:
@@ -409,10 +412,14 @@ class Cache:
             raise ValueError(f"{name} holds values out of range")
         return ptr, total, a
 
-    def _rows(self, t, name, total, heads):
-        """Packed rows [tokens][heads][head_dim] as the C ABI's hikv_rows."""
-        import torch
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    def _rows(self, i, t, name, total, heads):
+        """Packed rows [tokens][heads][head_dim] as the C ABI's hikv_rows: a
+        reference to the i-th of the structures kept for this cache's calls."""
+        try:
+            cuda = t.is_cuda
+        except AttributeError:
+            cuda = False
+        if not cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.get_device() != self.device_index:
             raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device_index}")
@@ -421,7 +428,9 @@ class Cache:
         stride = t.stride()
         if stride[2] != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        return hikv_rows(t.data_ptr(), stride[0], stride[1])
+        r = self._row_args[i]
+        r.data, r.token_stride, r.head_stride = t.data_ptr(), stride[0], stride[1]
+        return self._row_refs[i]
 
     def append_packed(self, k, v, ntok, layer=0, q=None, q_out=None, rope=None, stream=None):
         """Append a packed batch to one layer: k, v [sum ntok][Hkv][d] (any
@@ -431,19 +440,17 @@ class Cache:
         be q itself)."""
         c = self.cfg
         n, total, _keep = self._counts(ntok, "ntok")
-        rk, rv = self._rows(k, "k", total, c.num_kv_heads), self._rows(v, "v", total, c.num_kv_heads)
+        rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
         rq = ro = rc = None
         if q is not None:
-            rq = ctypes.byref(self._rows(q, "q", total, c.num_q_heads))
-            ro = ctypes.byref(self._rows(q_out, "q_out", total, c.num_q_heads))
+            rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, q_out, "q_out", total, c.num_q_heads)
         if rope is not None:
             if rope.device_index != self.device_index:
                 raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
-            rc = ctypes.byref(rope.c)
-        _check(_lib.hikv_append_packed(self.h, layer, n, ctypes.byref(rk), ctypes.byref(rv), rq, ro, rc,
-                                       self._stream_int(stream)))
+            rc = rope.ref
+        _check(_lib.hikv_append_packed(self.h, layer, n, rk, rv, rq, ro, rc, self._stream_int(stream)))
 
     def attend_packed(self, q, out, nq, layer=0, stream=None):
         """Causal attention of the newest nq[b] positions of every sequence
@@ -451,9 +458,8 @@ class Cache:
         (any 16-byte strides).  Append the positions' tokens first."""
         c = self.cfg
         n, total, _keep = self._counts(nq, "nq")
-        rq, ro = self._rows(q, "q", total, c.num_q_heads), self._rows(out, "out", total, c.num_q_heads)
-        _check(_lib.hikv_attend_packed(self.h, layer, n, ctypes.byref(rq), ctypes.byref(ro),
-                                       self._stream_int(stream)))
+        rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
+        _check(_lib.hikv_attend_packed(self.h, layer, n, rq, ro, self._stream_int(stream)))
 
     def drop(self, counts=None, layer0=0, nlayers=None, stream=None):
         """Drop the newest counts[b] tokens of every unit of batch row b (-1,
