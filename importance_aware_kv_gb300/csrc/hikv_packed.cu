@@ -32,6 +32,22 @@ const char* rows_fault(const hikv_cache* c, const hikv_rows* r, int64_t total, i
     return nullptr;
 }
 
+// Whether rows that are written may share memory with rows that are read: not
+// if their extents are apart, nor if they are slices of one buffer (equal
+// strides) that keep to their own part of the longer stride.
+bool rows_meet(const hikv_cache* c, const hikv_rows* w, int wh, const hikv_rows* r, int rh, int64_t total) {
+    auto extent = [&](const hikv_rows* x, int h) { return (total - 1) * x->token_stride + (h - 1) * x->head_stride + c->d; };
+    const int64_t at = ((int64_t)(uintptr_t)r->data - (int64_t)(uintptr_t)w->data) / c->esz;   // r's start from w's
+    if (at >= extent(w, wh) || -at >= extent(r, rh)) return false;
+    if (w->token_stride != r->token_stride || w->head_stride != r->head_stride) return true;
+    const bool by_token = w->token_stride >= w->head_stride;
+    const int64_t period = by_token ? w->token_stride : w->head_stride;
+    if (period == 0) return true;
+    auto part = [&](int h) { return (by_token ? (h - 1) * w->head_stride : (total - 1) * w->token_stride) + c->d; };
+    const int64_t off = (at % period + period) % period;
+    return off < part(wh) || period - off < part(rh);
+}
+
 RowsArg rows_arg(const hikv_cache* c, const hikv_rows* r) {
     return {(uint8_t*)r->data, r->token_stride * c->esz, r->head_stride * c->esz};
 }
@@ -221,6 +237,9 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
             return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out has %s", bad);
         if (q->data == q_out->data && (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
             return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out in the place of q needs its strides");
+        if ((q->data != q_out->data && rows_meet(c, q_out, c->Hq, q, c->Hq, total)) ||
+            rows_meet(c, q_out, c->Hq, k, c->Hkv, total) || rows_meet(c, q_out, c->Hq, vv, c->Hkv, total))
+            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out overlaps q, k or v");
     }
     if (rope) {
         if (!rope->cos || !rope->sin || (((uintptr_t)rope->cos | (uintptr_t)rope->sin) & 15))
@@ -330,7 +349,7 @@ hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, 
     const char* bad = nullptr;
     if ((bad = rows_fault(c, q, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
     if ((bad = rows_fault(c, out, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out has %s", bad);
-    if (q->data == out->data) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out aliases q");
+    if (rows_meet(c, out, c->Hq, q, c->Hq, total)) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out overlaps q");
     const int u0 = layer * c->per_layer;
     for (int i = 0; i < c->per_layer; ++i)
         if (nq[i / c->Hkv] > c->tail[u0 + i])

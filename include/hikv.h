@@ -338,7 +338,7 @@ typedef struct {
  * holds what it held at the capture (with a hikv_drop captured in front, say).
  * Errors: INVALID_ARG (null or misaligned pointers, strides, ntok < 0, a rope
  * whose table ends before the last position, q_out rows that overlap one
- * another), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append). */
+ * another, or q, k or v), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append). */
 hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* ntok_host,
                                const hikv_rows* k, const hikv_rows* v, const hikv_rows* q,
                                const hikv_rows* q_out, const hikv_rope* rope, hikv_stream_t stream);
@@ -362,7 +362,8 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
  * out: [sum nq][Hq] rows, written; must not overlap q.  Always exact
  * attention, with an element_budget too.  May be captured as
  * hikv_append_packed.
- * Errors: INVALID_ARG (null or misaligned pointers, strides, nq < 0), STATE
+ * Errors: INVALID_ARG (null or misaligned pointers, strides, nq < 0, rows of
+ * out that overlap one another or q's), STATE
  * (more queries than the unit holds newest positions in order: the tokens it
  * holds, or those appended since its last cut). */
 hikv_status hikv_attend_packed(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const hikv_rows* q,

@@ -704,3 +704,37 @@ def test_refusals_leave_the_cache_as_it_was(hk):
     cache.close()
     with pytest.raises(hk.HikvError):
         cache.attend_packed(q, qo, [1, 3])
+
+
+def test_overlapping_rows_are_refused_and_slices_are_not(hk):
+    """Written rows that share memory with rows that are read are refused; slices
+    of one buffer, tokens or heads outermost, are not."""
+    gen = gen_of(101)
+    cache = make(hk, 1, 4, 2, 64, "bf16", 400)
+    cos, sin = tables(400, 64)
+    rope = hk.Rope(cos, sin)
+    t = 20
+    buf = rnd(gen, t + 1, 8, 64)
+    q, k, v = buf[:t, :4], buf[:t, 4:6], buf[:t, 6:]
+    for bad in (buf[1:, :4], buf[:t, 1:5], buf[:t, 2:6], buf[:t, 4:], buf[1:, 3:7],
+                buf.view(-1)[64:64 + t * 256].view(t, 4, 64)):
+        with pytest.raises(hk.HikvError) as ei:
+            cache.append_packed(k, v, [t], q=q, q_out=bad, rope=rope)
+        assert ei.value.status == hk.HIKV_ERR_INVALID_ARG
+    heads = rnd(gen, 8, t, 64).transpose(0, 1)     # head outermost
+    cache.append_packed(heads[:, 4:6], heads[:, 6:], [t], q=heads[:, :4], q_out=heads[:, :4], rope=rope)
+    cache.append_packed(k, v, [t], q=q, q_out=q, rope=rope)
+    for out in (buf[1:, :4], buf[:t, 1:5], q):
+        with pytest.raises(hk.HikvError) as ei:
+            cache.attend_packed(q, out, [t])
+        assert ei.value.status == hk.HIKV_ERR_INVALID_ARG
+    q2 = q.clone()
+    out = buf[:t, 4:]                              # beside q in its own buffer
+    cache.attend_packed(q, out, [t])
+    assert torch.equal(q, q2)
+    check_attend(cache, q2, out, [t])
+    one = rnd(gen, 1, 8, 64)
+    cache.append_packed(one[:, 4:6], one[:, 6:], [1], q=one[:, :4], q_out=one[:, :4], rope=rope)
+    cache.attend_packed(one[:, :4], one[:, 4:], [1])
+    check_attend(cache, one[:, :4], one[:, 4:], [1])
+    cache.device_status()
