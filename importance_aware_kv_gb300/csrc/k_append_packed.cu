@@ -91,8 +91,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_append_packed(const __grid_c
     const int32_t tok = gw / a.slices, slice = gw - tok * a.slices;
     const int32_t t = a.seqs.start[0] + tok;
     griddep_launch_dependents();
-    griddep_wait();   // the rows' producer, and whoever still reads the pages
-    if (t >= a.seqs.start[a.seqs.n]) return;
     const int32_t b = prefix_find(a.seqs.start, a.seqs.n, t);
     const int32_t u0 = a.u0 + (a.seqs.row0 + b) * v.hkv;
     const int32_t i = t - a.seqs.start[b], ntok = a.seqs.start[b + 1] - a.seqs.start[b];
@@ -104,6 +102,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_append_packed(const __grid_c
     const int32_t y1 = rotates ? (INTER ? x1 + 16 : x1 + 16 * turned) : x1 + 16;
     const int32_t x0 = 32 * pair, y0 = x0 + 16;
     float c[VE], s[VE];
+    // (so far all of it was launch parameters)
+    griddep_wait();   // the rows' producer, and whoever still reads the pages
+    if (t >= a.seqs.start[a.seqs.n]) return;
     if (rotates) {
         const float* cp = a.cos + (int64_t)p * (a.rot / 2) + VE * pair;
         const float* sp = a.sin + (int64_t)p * (a.rot / 2) + VE * pair;
