@@ -1,0 +1,102 @@
+"""GPU tests of the packed-batch entry points at the edges of what they take:
+keys on both sides of every page, tile, split and causal edge, values near the
+ends of the number range, and an unread time-out.
+
+Bounds on the attention's error (notation of test_gpu_packed.py: h half a step
+of the cache dtype, u = 2^-24, e the error of a logit, p the exact weights, o
+the exact output).  Numerator and denominator are sums of the weights
+p_j (1 + a_j), |a_j| <= a = expm1(2 e) + 8 u, and sum_j p_j (v_j - o) = 0, so
+these errors move a row only as far as its values differ.  bf16 rounds the
+weights of the numerator once more, by h (fp32: g = 0, else g = h), and takes
+the rounded value of the largest, p_m, into the denominator as well:
+    |out - o| <= [a sum_j p_j |v_j - o|
+                  + g (p_m |v_m - o| + sum_{j != m} p_j |v_j|)] / (1 - a - g)
+                 + 2 n u sum_j p_j |v_j| + h |o|.
+Norm-wise, with independent roundings of variance below h^2,
+    |out - o|^2 <= 2 sum [g^2 (p_m^2 (v_m - o)^2 + sum_{j != m} p_j^2 v_j^2)
+                          + a^2 sum_j p_j^2 (v_j - o)^2 + h^2 o^2]
+                   + sum [n u (|o| + 4 sqrt(sum_j p_j^2 v_j^2))]^2
+(the factor 2 on top of a variance that is at most a third of h^2; the last
+term: n additions that each lose u of a partial sum, partial sums at most four
+times their random-walk size).
+"""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_packed import DEV, DT, HALF, U, gen_of, hk, make, rnd, slots  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def check_edges(cache, q, out, nq, layer=0, norm=False):
+    """out against attention in 64 bits by the bounds above, element by element
+    or (norm) over all rows of a sequence and KV head."""
+    c = cache.cfg
+    dtype, d, hkv, G = c.dtype, c.head_dim, c.num_kv_heads, c.num_q_heads // c.num_kv_heads
+    scale = c.scale or 1.0 / math.sqrt(d)
+    h, gp = HALF[dtype], HALF[dtype] if dtype == "bf16" else 0.0
+    r = 0
+    for b, t in enumerate(nq):
+        for g in range(hkv if t else 0):
+            k, v, pos = slots(cache, (layer * c.batch + b) * hkv + g)
+            n = k.shape[0]
+            newest = int(pos.max())
+            kd, vd = k.double(), v.double()
+            total = limit = 0.0
+            for i0 in range(0, t, 64):
+                m = min(64, t - i0)
+                x = q[r + i0:r + i0 + m, g * G:(g + 1) * G].double()
+                z = torch.einsum("mgd,nd->mgn", x, kd) * scale
+                e = 2 * d * U * scale * torch.einsum("mgd,nd->mgn", x.abs(), kd.abs()).amax(-1)
+                mine = newest - t + 1 + i0 + torch.arange(m, device=DEV)
+                p = torch.softmax(z.masked_fill(~(pos[None] <= mine[:, None])[:, None], -math.inf), -1)
+                o = p @ vd
+                a = (torch.expm1(2 * e) + 8 * U)[..., None]
+                pm, m_at = p.max(-1, keepdim=True)
+                vm = vd[m_at[..., 0]]
+                err = (out[r + i0:r + i0 + m, g * G:(g + 1) * G].double() - o).abs()
+                if norm:
+                    p2 = p * p
+                    v2 = p2 @ (vd * vd)
+                    spread = v2 - 2 * o * (p2 @ vd) + p2.sum(-1, keepdim=True) * o * o
+                    rounded = v2 + pm * pm * ((vm - o).square() - vm.square())
+                    limit += float((2 * (gp * gp * rounded + a * a * spread + h * h * o * o)).sum())
+                    limit += float((n * U * (o.abs() + 4 * v2.sqrt())).square().sum())
+                    total += float(err.square().sum())
+                    continue
+                spread = torch.stack([(p * (vd[:, j] - o[..., j:j + 1]).abs()).sum(-1) for j in range(d)], -1)
+                mag = p @ vd.abs()
+                rounded = mag + pm * ((vm - o).abs() - vm.abs())
+                tol = ((a * spread + gp * rounded) / (1 - a - gp) + 2 * n * U * mag) * (1 + h) + h * o.abs()
+                assert bool((err <= tol).all()), (b, g, i0, float((err - tol).max()), int((~(err <= tol)).sum()))
+            assert not norm or total <= limit, (b, g, total, limit)
+        r += t
+
+
+# ---------------------------------------------------------------------------
+# values of every size
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("at", [5, 200, 290])
+def test_a_row_that_sees_one_key_returns_its_value(hk, dtype, d, at):
+    """One key has all but 300 e^-14 = 0.00025 of a row's weight: the rounding
+    of its probability, 2^-8, is in numerator and denominator alike."""
+    gen = gen_of(111 + at)
+    n, t = 300, 8
+    cache = make(hk, 1, 8, 2, d, dtype, n, scale=1.0)
+    k = torch.zeros(n, 2, d, device=DEV)
+    k[at, :, 0] = 14.0
+    v = rnd(gen, n, 2, d, dtype=dtype)
+    cache.append_packed(k.to(DT[dtype]), v, [n])
+    q = torch.zeros(t, 8, d, device=DEV)
+    # logits 14 to 16.3, all bf16 steps of their binade among them; log2 of the weights 20.2 to 23.4
+    q[..., 0] = 1.0 + torch.arange(t * 8, device=DEV).view(t, 8) / 384.0
+    q = q.to(DT[dtype])
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, [t])
+    check_edges(cache, q, out, [t])
+    cache.device_status()
+
+
