@@ -76,6 +76,78 @@ def check_edges(cache, q, out, nq, layer=0, norm=False):
 
 
 # ---------------------------------------------------------------------------
+# every key once: no key missed, taken twice, or seen too early
+# ---------------------------------------------------------------------------
+def needles(gen, cache, held, new, hq, hkv, d, dtype):
+    """Keys of +-1; each query points at two of them with equal logits that
+    outweigh all others together: one at an edge and another, far from it.  A
+    missed edge key leaves the other's value, one taken twice weighs 2 : 1, and
+    a key behind the causal limit shows where the other alone should."""
+    lens = [a + b for a, b in zip(held, new)]
+    ks = []
+    for n in (held, new):
+        t = sum(n)
+        k = torch.randint(0, 2, (t, hkv, d), generator=gen, device=DEV).mul(2).sub(1).to(DT[dtype])
+        cache.append_packed(k, rnd(gen, t, hkv, d, dtype=dtype), n)
+        ks.append(k.split(n))
+    keys = [torch.cat([a, b]) for a, b in zip(*ks)]
+    # slots on both sides of every 16 (pages, tiles of 64 and 128 keys and parts of the keys begin at some)
+    edges = [sorted({s for x in range(0, n + 1, 16) for s in (x - 1, x) if 0 <= s < n}) for n in lens]
+    G = hq // hkv
+    at = 0
+    while at < max(len(e) for e in edges):
+        q = torch.empty(sum(new), hq, d, device=DEV)
+        r = 0
+        for b, t in enumerate(new):
+            e = torch.tensor(edges[b], device=DEV)
+            i = torch.arange(t, device=DEV)[:, None].expand(t, G)
+            lim = held[b] + i
+            a = e[(at + torch.arange(t * G, device=DEV).view(t, G)) % len(e)]
+            # the first two heads also look at the causal limit and right behind it
+            a[:, 0] = torch.where(torch.arange(t, device=DEV) % 2 == at % 2, lim[:, 0], a[:, 0])
+            if G > 1:
+                a[:, 1] = (lim[:, 1] + 1).clamp(max=lens[b] - 1)
+            # (the other is always visible: an edge key may not be)
+            other = (a + 37 + lens[b] // 2) % (held[b] + i + 1)
+            for g in range(hkv):
+                q[r:r + t, g * G:(g + 1) * G] = keys[b][a, g].float() + keys[b][other, g].float()
+            r += t
+        at += sum(new) * G if sum(new) else 1
+        yield (2 * q).to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("bf16", 128, 8, 1), ("bf16", 64, 4, 2), ("bf16", 128, 2, 2),
+                                            ("f32", 64, 4, 2)])
+@pytest.mark.parametrize("new,held,page", [([17], [9000], 64), ([40, 1], [5000, 300], 16), ([3, 5], [2000, 2500], 128),
+                                           ([130], [1000], 64), ([300, 129], [0, 140], 32), ([700], [0], 256)])
+def test_every_edge_key_counts_once(hk, dtype, d, hq, hkv, new, held, page):
+    gen = gen_of(sum(held) + d + hq)
+    cap = max(a + b for a, b in zip(new, held))
+    cache = make(hk, len(new), hq, hkv, d, dtype, cap, page_tokens=page, scale=0.25 if d == 64 else 0.125)
+    out = torch.empty(sum(new), hq, d, device=DEV, dtype=DT[dtype])
+    for q in needles(gen, cache, held, new, hq, hkv, d, dtype):
+        cache.attend_packed(q, out, new)
+        check_edges(cache, q, out, new)
+    cache.device_status()
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("bf16", 64, 8, 1), ("f32", 64, 4, 2)])
+@pytest.mark.parametrize("new,held", [([17], [19000]), ([64], [9000]), ([40, 3], [5000, 2000]), ([1000], [0]), ([300, 200], [700, 31])])
+def test_error_over_many_keys_is_that_of_rounding(hk, dtype, d, hq, hkv, new, held):
+    """Norm-wise: a key or a tile of keys lost somewhere in a long cache is larger than the rounding."""
+    gen = gen_of(sum(held) + sum(new) + d)
+    cap = max(a + b for a, b in zip(new, held))
+    cache = make(hk, len(new), hq, hkv, d, dtype, cap)
+    for n in (held, new):
+        cache.append_packed(rnd(gen, sum(n), hkv, d, dtype=dtype), rnd(gen, sum(n), hkv, d, dtype=dtype), n)
+    q = rnd(gen, sum(new), hq, d, dtype=dtype)
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, new)
+    cache.device_status()
+    check_edges(cache, q, out, new, norm=True)
+
+
+# ---------------------------------------------------------------------------
 # values of every size
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
