@@ -135,7 +135,7 @@ struct AttendArgs {
     float qscale;           // scale * log2(e)
     int32_t chunk;          // keys per split (a multiple of the kernel's key tile)
     float* part;            // partial results of split items: [splits][part_rows][d] outputs, ...
-    float* part_ml;         // ... [splits][part_rows][2] maxima and sums
+    float* part_ml;         // ... [splits][part_rows][2] references and sums
     int64_t part_rows;      // rows (t, h) of the packed batch
     int32_t splits;         // the most parts a sequence's keys are split into
     int32_t hkv_shift;      // log2 of the KV heads, -1: no power of two

@@ -6,9 +6,9 @@ namespace hikv {
 namespace {
 
 // Warp per query row (t, h) of the sequences that were split, a lane per
-// split first: with m the largest of the partial maxima and f_s = 2^(m_s - m),
+// split first: with m_s the parts' references, m the largest and f_s = 2^(m_s - m),
 //   o = sum_s f_s O_s / sum_s f_s l_s.
-// Bound by the latency of its three dependent reads (length, maxima, parts).
+// Bound by the latency of its three dependent reads (length, references, parts).
 template <typename T, int D>
 __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a) {
     constexpr int E = D / 32;   // elements of a lane

@@ -4,13 +4,16 @@
 //   o_i = sum_{s <= lim_i} 2^(t_is - m_i) v_s / sum_{s <= lim_i} 2^(t_is - m_i),
 //   t_is = scale log2(e) q_i . k_s,
 //
-// in one pass over the keys.  The exponent's reference m_i is a running
-// maximum that moves only when a tile's maximum passes it by more than 24 (in
-// powers of two): until then 2^(t - m) <= 2^24, which fp32 sums of 2^20 keys
-// and the bf16 probabilities hold at their full relative precision, and the
-// accumulator needs no rescaling.  (A step of 8 moves it in one tile of
-// twenty for heavy-tailed logits, and one row that moves holds up its whole
-// tile: 2650 us against 2575 for 16K tokens of 64/8 heads.)
+// in one pass over the keys.  The exponent's reference m_i lies up to 24 (in
+// powers of two) above the running maximum and moves only when a tile's
+// maximum passes it: until then the accumulator needs no rescaling.  The
+// largest weight of a row is then in [2^-24, 1], so that sums of n weighted
+// values stay below n max |v|, as with a reference at the maximum, and bf16 and
+// fp32 hold weights and sums at their full relative precision (a product of a
+// weight and a value below 2^-126, |v| < 2^-102, may be lost).  (A step of 8
+// moves it in one tile of twenty for heavy-tailed logits, and one row that
+// moves holds up its whole tile: 2650 us against 2575 for 16K tokens of 64/8
+// heads.)
 //
 // A CTA takes one work item after the other, 256 query rows x one KV head: two
 // tiles of 128 rows that share every key tile, so that the tensor cores work
@@ -34,7 +37,7 @@
 // averaged over the keys).  The sums l are of the fp32 values, but for a row's
 // largest probability (the largest between two moves of the reference), which
 // enters rounded there too: a row that sees little else returns that key's value
-// as it is, wherever in [1, 2^24] the lagging reference has left its
+// as it is, wherever in [2^-24, 1] the reference has left its
 // probability.  (Against 64 bits the 8K prompt is off by 0.0019 norm-wise,
 // 0.0023 without this; summing every rounded value gives 0.0019 too and takes
 // 358 us instead of 350.)
@@ -58,6 +61,7 @@ constexpr int kThreads = 384;
 // 256 x 216 + 128 x 72 = 384 x 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr int kKeys = kTcKeys, kRows = kTcRows;
+constexpr float kAhead = 24.f;   // the reference above the maximum that it was set at
 
 template <int D>
 struct Tc {
@@ -287,10 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t lim = w.seen0 + (rc >> a.gshift);   // this row sees slots [0, lim]
             const int32_t lim_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3), w.rows - 1) >> a.gshift);
             const int32_t nt = tile ? w.nt1 : w.nt0;
-            float m = -INFINITY, l = 0.f;
-            float top = -INFINITY;   // the largest logit since m last moved
-            auto settle = [&] {      // its probability in l as the product took it (1 if it is m)
-                const float pt = ex2(fmaf(top, c, m == -INFINITY ? 0.f : -(m * c)));
+            float m = -INFINITY, l = 0.f;   // m: the maximum at the reference's last move
+            float top = -INFINITY;          // the largest logit since
+            auto reference = [&] { return m == -INFINITY ? 0.f : fmaf(m, c, kAhead); };
+            auto settle = [&] {             // top's probability in l as the product took it
+                const float pt = ex2(fmaf(top, c, -reference()));
                 l += __uint_as_float(pack_bf16x2(pt, 0.f) << 16) - pt;
             };
             for (int32_t t = 0; t < nt; ++t) {
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
                 const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 // (mt - m is NaN while both are -inf: no move)
-                const bool move = (mt - m) * c > 24.0f;
+                const bool move = (mt - m) * c > kAhead;
                 if (__any_sync(0xffffffffu, move)) {
                     const float f = m == mt ? 1.f : ex2((m - mt) * c);
                     if (t > 0) {
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = m = mt;
                 }
                 top = fmaxf(top, mt);
-                const float base = m == -INFINITY ? 0.f : m * c;
+                const float base = reference();
                 const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.split >= 0 && row < w.rows) {
                     const int32_t tok = w.first + (row >> a.gshift), h = (w.g << a.gshift) + (row & ((1 << a.gshift) - 1));
                     const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h;
-                    *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
+                    *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m == -INFINITY ? m : reference(), l);
                 }
             }
             __syncwarp();

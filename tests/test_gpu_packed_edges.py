@@ -172,3 +172,29 @@ def test_a_row_that_sees_one_key_returns_its_value(hk, dtype, d, at):
     cache.device_status()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("size", [1e-25, 1e33, 1e36])
+@pytest.mark.parametrize("held", [0, 6000])
+def test_values_whose_mean_is_finite(hk, dtype, d, size, held):
+    """Logits that grow along the keys by up to 23 in powers of two, and values
+    so large that the weights have to stay near one for sums to be finite:
+    |v| <= 5 x 10^36, at most 64 keys near the maximum."""
+    gen = gen_of(121)
+    n, t = held + 300, 9
+    cache = make(hk, 1, 8, 2, d, dtype, n, scale=1.0)
+    k = torch.full((n, 2, d), 0.0, device=DEV)
+    k[:, :, 0] = -30.0
+    k[:held + 64, :, 0] = torch.linspace(-40.0, 0.0, held + 64, device=DEV)[:, None]
+    k[held + 140:held + 200, :, 0] = 15.0
+    v = (rnd(gen, n, 2, d, dtype="f32") * size).to(DT[dtype])
+    cache.append_packed(k.to(DT[dtype]), v, [n])
+    q = torch.zeros(t, 8, d, device=DEV)
+    q[..., 0] = 1.0 - torch.arange(t * 8, device=DEV).view(t, 8) / 100.0
+    q = q.to(DT[dtype])
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, [t])
+    assert bool(torch.isfinite(out).all())
+    check_edges(cache, q, out, [t])
+    cache.device_status()
+
+
