@@ -24,7 +24,7 @@
 // long as one of 128 columns would (its rows' operand, 4 KB, comes at 64 bytes a
 // cycle), so a 128 x 64 tile's S takes 3,500 cycles and its P V 1,536 of the
 // 5,800 a step; 128 keys a tile would need 544 columns of tensor memory.
-// 4096 tokens with 32/8 heads, d = 128: 688 us, 200 TFLOP/s of fp32 work (the same
+// 4096 tokens with 32/8 heads, d = 128: 695 us, 198 TFLOP/s of fp32 work (the same
 // on the CUDA cores, 4 x 4 tiles in registers: 2,947 us, 46.7).
 //
 // Non-finite V elements do not go through the products (0 x inf): they are
@@ -62,13 +62,17 @@ struct F3 {
 // columns of tensor memory: three parts of Q, S, three parts of P, O
 constexpr int kTmQ = 0, kTmS = 192, kTmP = 256, kTmO = 352;
 
-// magnitudes that round to a bf16 infinity, and NaN
+// magnitudes that round to a bf16 infinity (the finite ones from 0x7F7F8000 on too), and NaN
 __device__ __forceinline__ bool rounds_to_inf(float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F7F8000u; }
+__device__ __forceinline__ bool non_finite(float x) { return (__float_as_uint(x) & 0x7FFFFFFFu) >= 0x7F800000u; }
 
-// two fp32 values as three packed bf16 pairs; each remainder is exact in fp32
+// Two fp32 values as three packed bf16 pairs; each remainder is exact in fp32.
+// CUT: the first part cut off instead of rounded, for values that would round to
+// infinity (the parts still hold 24 bits between them; NaN stays NaN in each).
+template <bool CUT = false>
 __device__ __forceinline__ void three_parts(float2 x, uint32_t& h, uint32_t& m, uint32_t& l) {
     const float2 minus = make_float2(-1.f, -1.f);
-    h = pack_bf16x2(x.x, x.y);
+    h = CUT ? __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632) : pack_bf16x2(x.x, x.y);
     const float2 r = ffma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)), minus, x);
     m = pack_bf16x2(r.x, r.y);
     const float2 q = ffma2(make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), minus, r);
@@ -86,7 +90,7 @@ __device__ __forceinline__ void put_parts(uint8_t* at, int stride, float* x, F m
     if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
         mend(x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) three_parts(make_float2(x[2 * i], x[2 * i + 1]), h[i], m[i], l[i]);
+        for (int i = 0; i < 4; ++i) three_parts<true>(make_float2(x[2 * i], x[2 * i + 1]), h[i], m[i], l[i]);
     }
     *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(at + stride) = make_uint4(m[0], m[1], m[2], m[3]);
@@ -96,7 +100,7 @@ __device__ __forceinline__ void put_parts(uint8_t* at, int stride, float* x, F m
 __device__ __forceinline__ void mark_nan(float* x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (rounds_to_inf(x[i])) x[i] = __int_as_float(0x7FC00000);
+        if (non_finite(x[i])) x[i] = __int_as_float(0x7FC00000);
 }
 
 template <int D>
@@ -192,9 +196,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                     mark_nan(x);
                     mark_nan(x + 8);
                 }
+                bool big = false;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) big |= rounds_to_inf(x[k]);
                 uint32_t hi[8], mi[8], lw[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) three_parts(make_float2(x[2 * k], x[2 * k + 1]), hi[k], mi[k], lw[k]);
+                if (big) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) three_parts<true>(make_float2(x[2 * k], x[2 * k + 1]), hi[k], mi[k], lw[k]);
+                }
                 const uint32_t tq = tmem + base_lane + kTmQ + 8 * j;
                 tmem_st8(tq, hi);
                 tmem_st8(tq + D / 2, mi);
@@ -384,12 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                         if (!is_v) return mark_nan(y);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            if (!rounds_to_inf(y[k])) continue;
+                            if (!non_finite(y[k])) continue;
                             const int kind = y[k] != y[k] ? 2 : (y[k] < 0.f ? 1 : 0);
                             atomicMin(&over[kind * D + 8 * chunk + k], s0 + r);
                             y[k] = 0.f;
+                            misc[1] = 1;
                         }
-                        misc[1] = 1;
                         __threadfence_block();
                     };
                     put_parts(tile + place(chunk, r, C::KBLOCK), C::KPART, x[j], mend);

@@ -198,3 +198,28 @@ def test_values_whose_mean_is_finite(hk, dtype, d, size, held):
     cache.device_status()
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 1)])
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+@pytest.mark.parametrize("value", [3.3895314e38, 3.3961775e38, 3.3999e38, 3.4028234663852886e38, -3.4028234663852886e38])
+def test_the_largest_fp32_numbers_are_numbers(hk, d, hq, hkv, where, value):
+    """Elements of q, k and v up to the largest finite one, whose nearest bf16
+    is an infinity: against 2^-124 in a logit, and as one value among others."""
+    gen = gen_of(131)
+    n = 150
+    cache = make(hk, 1, hq, hkv, d, "f32", n)
+    k, v, q = rnd(gen, n, hkv, d, dtype="f32"), rnd(gen, n, hkv, d, dtype="f32"), rnd(gen, n, hq, d, dtype="f32")
+    if where == "v":
+        v[70, :, 5] = value
+    else:
+        big, small = (q, k) if where == "q" else (k, q)
+        big[..., 3] = 0.0
+        big[70, :, 3] = value
+        small[..., 3] = 2.0 ** -124
+    cache.append_packed(k, v, [n])
+    out = torch.empty_like(q)
+    cache.attend_packed(q, out, [n])
+    assert bool(torch.isfinite(out).all())
+    check_edges(cache, q, out, [n])
+    cache.device_status()
+
+
