@@ -1061,7 +1061,10 @@ hikv_status hikv_selftest_timeout(hikv_cache* c, int32_t limit_us, hikv_stream_t
     pdl_forget(c);
     if (!c || limit_us < 1 || limit_us > 2000000)
         return fail(HIKV_ERR_INVALID_ARG, "selftest_timeout: bad cache or limit");
-    cudaError_t e = launch_selftest_timeout(c->v, (uint64_t)limit_us * 1000u, (cudaStream_t)stream);
+    const char* site = std::getenv("HIKV_SELFTEST_SITE");
+    const bool attend = site && std::atoi(site) == (int)kWaitAttend;
+    cudaError_t e = (attend ? launch_selftest_attend : launch_selftest_timeout)(c->v, (uint64_t)limit_us * 1000u,
+                                                                                 (cudaStream_t)stream);
     c->launches += 1;
     if (e != cudaSuccess) return cuda_fail(e, "selftest_timeout: launch");
     return HIKV_OK;

@@ -7,6 +7,31 @@
 namespace hikv {
 
 enum : uint32_t { kWaitAttend = 9 };   // the next kWait* code: packed attention
+// the next DEVERR_* bit: a wait of packed attention gave up (its launches start
+// nothing more until the error is read: each work item would wait as long)
+enum : uint32_t { DEVERR_ATTEND = 16u };
+// A wait of these kernels, bounded as mbar_wait_bounded.  Where one gives up, it
+// notes that in the CTA's word `where` (zero at first), which one thread records at
+// the end: recording at each wait made the kernels 1 to 3 % slower.
+__device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* where, uint32_t index,
+                                            uint64_t limit_ns = kWaitLimitNs) {
+    if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0; i < (1u << 24); ++i) {
+        if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
+        if ((i & 63u) == 63u && global_ns() - t0 > limit_ns) break;
+    }
+    *where = index;
+    return false;
+}
+__device__ __forceinline__ void attend_record(uint32_t* err, uint32_t where, uint64_t limit_ns = kWaitLimitNs) {
+    if (where == 0) return;
+    atomicOr(err, DEVERR_ATTEND);
+    record_timeout(err, kWaitAttend, where, limit_ns);
+}
+__device__ __forceinline__ bool attend_gave_up(const View& v) {
+    return (*reinterpret_cast<const volatile uint32_t*>(v.err) & DEVERR_ATTEND) != 0;
+}
 
 // Address of the K (or V) row of slot s of unit u through unit_page (no table
 // read with home pages); nullptr if the page is bad.
@@ -168,6 +193,7 @@ constexpr int kTcRows = 256, kTcKeys = 128;    // query rows of a work item of t
 cudaError_t launch_attend_f32(const AttendArgs& a, int d, cudaStream_t s);
 constexpr int kF32Rows = 128, kF32Keys = 64;   // of the fp32 kernel
 cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s);
+cudaError_t launch_selftest_attend(const View& v, uint64_t limit_ns, cudaStream_t s);
 
 constexpr int kDropMax = 512;
 struct DropArgs {

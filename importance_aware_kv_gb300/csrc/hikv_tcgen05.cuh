@@ -114,8 +114,8 @@ __device__ __forceinline__ bool elect_one() {
     return e != 0;
 }
 // a bounded wait of a whole warp: all lanes agree on the outcome
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t index) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, kWaitAttend, index));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* where, uint32_t index) {
+    return __all_sync(0xffffffffu, attend_wait(bar, parity, where, index));
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -125,14 +125,14 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // a turn between the two issuing threads (it orders no memory)
-__device__ __forceinline__ bool turn_begin(uint32_t* turn, uint32_t* err) {
+__device__ __forceinline__ bool turn_begin(uint32_t* turn, volatile uint32_t* where) {
     if (atomicExch(turn, 1u) == 0u) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t i = 0; i < (1u << 28); ++i) {
         if (atomicExch(turn, 1u) == 0u) return true;
         if ((i & 255u) == 255u && global_ns() - t0 > kWaitLimitNs) break;
     }
-    record_timeout(err, kWaitAttend, 0x508, global_ns() - t0);
+    *where = 0x508;
     return false;
 }
 __device__ __forceinline__ void turn_end(uint32_t* turn) { atomicExch(turn, 0u); }

@@ -56,6 +56,7 @@ struct F3 {
     // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_read, p_full, o_full, drained
     static constexpr int OFF_BAR = 4 * TILE;
     static constexpr int OFF_MISC = OFF_BAR + 14 * 8;     // tensor memory address, non-finite values noted
+    static constexpr int OFF_WHERE = OFF_MISC + 8;        // where a wait gave up
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     uint64_t* o_full = p_full + 1;
     uint64_t* drained = o_full + 1;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
+    volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_WHERE);
     int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
     const View& v = a.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
         mbar_init(o_full, 1);
         mbar_init(drained, 1);
         misc[1] = 0;
+        *where = 0;
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 3 * D; i += kThreads) over[i] = 0x7FFFFFFF;
@@ -160,11 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     const int32_t last_lim = seen0 + ((min(r0 + kRows, rows) - 1) >> a.gshift);   // what the last row sees
     const int32_t lo = splits > 1 ? split * a.chunk : 0;
     const int32_t end = splits > 1 ? min(last_lim + 1, lo + a.chunk) : last_lim + 1;
-    const volatile uint32_t* err = v.err;
     const bool sane = n >= nq && n <= v.cap;
     if (!sane && threadIdx.x == 0) atomicOr(v.err, DEVERR_STATE);
-    // (after a wait of these kernels gave up nothing more is started: each item would wait as long)
-    const bool bad = !sane || ((err[0] & DEVERR_TIMEOUT) != 0 && err[1] == kWaitAttend);
+    const bool bad = !sane || attend_gave_up(v);
     const int32_t nt = bad || end <= lo ? 0 : (end - lo + kKeys - 1) / kKeys;
 
     tc_fence_before();
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
         for (int j = 0; j < D / 2; ++j) acc[j] = make_float2(0.f, 0.f);
         // add the tile's P V
         auto add = [&](uint32_t parity) {
-            ok = warp_wait(o_full, parity, v.err, 0x800);
+            ok = warp_wait(o_full, parity, where, 0x800);
             if (!ok) return;
             tc_fence_after();
 #pragma unroll
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             }
         };
         for (int32_t t = 0; ok && t < nt; ++t) {
-            ok = warp_wait(s_full, t & 1, v.err, 0x801);
+            ok = warp_wait(s_full, t & 1, where, 0x801);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[64];
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             if (run) load(lo);
             for (int32_t t = 0; ok && t < nt; ++t) {
                 const int32_t s0 = lo + t * kKeys;
-                if (t > 1) ok = warp_wait((is_v ? v_empty : k_empty) + (t & 1), ((t - 2) >> 1) & 1, v.err, 0x802 + is_v);
+                if (t > 1) ok = warp_wait((is_v ? v_empty : k_empty) + (t & 1), ((t - 2) >> 1) & 1, where, 0x802 + is_v);
                 if (!ok) break;
                 uint8_t* tile = tiles0 + (t & 1) * C::TILE;
 #pragma unroll
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                 constexpr int PA[6] = {1, 0, 2, 0, 1, 0}, PB[6] = {1, 2, 0, 1, 0, 0};
                 bool ok = run;
                 auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t index) {
-                    ok = ok && mbar_wait_bounded(bar, parity, v.err, kWaitAttend, index);
+                    ok = ok && attend_wait(bar, parity, where, index);
                 };
                 auto qk = [&](int32_t t) {   // S of tile t
                     const uint64_t b = dk + (t & 1) * (C::TILE >> 4);
@@ -454,13 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                 }
                 // nothing is in flight when the CTA ends, after a wait that gave up neither
                 mma_commit(drained);
-                mbar_wait_bounded(drained, 0, v.err, kWaitAttend, 0x808);
+                attend_wait(drained, 0, where, 0x808);
             }
             __syncwarp();
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) attend_record(v.err, *where);
     if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

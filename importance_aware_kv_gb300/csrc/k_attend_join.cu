@@ -16,6 +16,7 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     const int32_t x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
+    const bool gave_up = attend_gave_up(v);   // parts are missing: write nothing
     const int32_t tok = x / v.hq, h = x % v.hq;
     if (tok >= a.comb0[a.nseq]) return;
     const int32_t i = prefix_find(a.comb0, a.nseq, tok);
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     }
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (gave_up) return;
     T* dst = reinterpret_cast<T*>(a.out.row(a.start[i] + j, h)) + lane * E;
 #pragma unroll
     for (int k = 0; k < E; ++k) dst[k] = Elem<T>::from_f(o[k] / l);
@@ -59,7 +61,25 @@ cudaError_t launch(const AttendArgs& a, int d, cudaStream_t s) {
                     : launch_overlapped(k_attend_join<T, 64>, grid, 128, 0, s, a);
 }
 
+// one CTA whose wait on a barrier that nothing arrives on gives up after limit_ns
+__global__ void k_selftest_attend(View v, uint64_t limit_ns) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ uint32_t where;
+    if (threadIdx.x == 0) {
+        where = 0;
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+        attend_wait(&bar, 0u, &where, 1u, limit_ns);
+        attend_record(v.err, where, limit_ns);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_selftest_attend(const View& v, uint64_t limit_ns, cudaStream_t s) {
+    k_selftest_attend<<<1, 32, 0, s>>>(v, limit_ns);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s) {
     return dtype == HIKV_BF16 ? launch<__nv_bfloat16>(a, d, s) : launch<float>(a, d, s);

@@ -78,7 +78,8 @@ struct Tc {
     static constexpr int OFF_ANSWER = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // of the work distributor, 16 bytes
     static constexpr int OFF_ITEM = OFF_ANSWER + 16;      // two work items
     static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item, turn
-    static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
+    static constexpr int OFF_WHERE = OFF_MISC + 16;       // where a wait gave up
+    static constexpr int OFF_OVER = OFF_WHERE + 16;       // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
 
@@ -155,12 +156,12 @@ struct Items {
     uint64_t* full;
     uint64_t* empty;
     const Item* slot;
-    uint32_t* err;
+    volatile uint32_t* where;
     uint32_t n = 0;   // number of the next item to take
     // the next item, false if there is none left; a whole warp
     __device__ __forceinline__ bool take(Item& w) {
         const uint32_t s = n & 1;
-        if (!warp_wait(&full[s], (n >> 1) & 1, err, 0x700)) return false;
+        if (!warp_wait(&full[s], (n >> 1) & 1, where, 0x700)) return false;
         w = slot[s];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
@@ -170,7 +171,7 @@ struct Items {
     // the same for one thread
     __device__ __forceinline__ bool take_one(Item& w) {
         const uint32_t s = n & 1;
-        if (!mbar_wait_bounded(&full[s], (n >> 1) & 1, err, kWaitAttend, 0x701)) return false;
+        if (!attend_wait(&full[s], (n >> 1) & 1, where, 0x701)) return false;
         w = slot[s];
         mbar_arrive(&empty[s]);
         ++n;
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* item_full = answer + 1;
     uint64_t* item_empty = item_full + 2;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
+    volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_WHERE);
     int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
     const View& v = a.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -245,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         misc[1] = 0;                      // epilogues done, in warps
         misc[3] = 0;                      // a row tile is issuing the products between two of its softmaxes
+        *where = 0;
         misc[2] = 0;                      // the item that `over` belongs to, from 1 on
         fence_mbar_init();
         prefetch_tensormap(&qmap);
@@ -256,23 +259,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // (a wait of this kernel gave up: start nothing more, each item would wait as long)
-    uint32_t err0 = 0, err1 = 0;
-    if (warp == 8) {
-        err0 = reinterpret_cast<const volatile uint32_t*>(v.err)[0];
-        err1 = reinterpret_cast<const volatile uint32_t*>(v.err)[1];
-    }
+    const bool gave_up = warp == 8 && attend_gave_up(v);
     griddep_wait();   // what the kernel before writes is there: lengths, pages, q
     Item w0;
     if (warp == 8) {
         if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
-        w0.some = !((err0 & DEVERR_TIMEOUT) != 0 && err1 == kWaitAttend);
+        w0.some = !gave_up;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    Items items{item_full, item_empty, reinterpret_cast<Item*>(sm + C::OFF_ITEM), v.err};
+    Items items{item_full, item_empty, reinterpret_cast<Item*>(sm + C::OFF_ITEM), where};
     Item w;
 
     if (warp < 8) {
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += __uint_as_float(pack_bf16x2(pt, 0.f) << 16) - pt;
             };
             for (int32_t t = 0; t < nt; ++t) {
-                if (!warp_wait(&s_full[tile], sphase, v.err, 0x100 + t)) { ok = false; break; }
+                if (!warp_wait(&s_full[tile], sphase, where, 0x100 + t)) { ok = false; break; }
                 sphase ^= 1;
                 tc_fence_after();
                 uint32_t s[128];
@@ -369,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             settle();
             if (nt > 0) {
-                if (!warp_wait(&o_full[tile], ophase, v.err, 0x200)) { ok = false; break; }
+                if (!warp_wait(&o_full[tile], ophase, where, 0x200)) { ok = false; break; }
                 ophase ^= 1;
                 tc_fence_after();
                 if (misc[2] == items.n) {
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto hand_out = [&](const Item& x) {
             const uint32_t s = n & 1;
-            if (n >= 2) ok = ok && warp_wait(&item_empty[s], ((n - 2) >> 1) & 1, v.err, 0x702);
+            if (n >= 2) ok = ok && warp_wait(&item_empty[s], ((n - 2) >> 1) & 1, where, 0x702);
             if (!ok) return;
             if (lane == 0) {
                 *reinterpret_cast<Item*>(sm + C::OFF_ITEM + 64 * s) = x;
@@ -465,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_item = [&](Item& x) {
             x.some = 0;
             while (ok) {
-                ok = warp_wait(answer, read & 1, v.err, 0x703);
+                ok = warp_wait(answer, read & 1, where, 0x703);
                 if (!ok) return;
                 ++read;
                 const int32_t it = read_next(ans);
@@ -494,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (x == fills || !ok) break;
                 if (x == 1) {   // the first keys wait for nothing
-                    if (loaded > 0) ok = warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x300);
+                    if (loaded > 0) ok = warp_wait(q_empty, (loaded - 1) & 1, where, 0x300);
                     if (!ok) break;
                     ++loaded;
                     const int tiles = w.r0 + 128 < w.rows ? 2 : 1;
@@ -509,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int st = fill % C::STAGES;
                 const uint32_t use = fill / C::STAGES;
-                if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, v.err, 0x400 + st)) { ok = false; break; }
+                if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, where, 0x400 + st)) { ok = false; break; }
                 ++fill;
                 const bool is_v = x & 1;
                 const int32_t s0 = w.lo + (x >> 1) * kKeys;
@@ -535,16 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             w = next;
         }
         // every answer and copy has landed and every commit arrived before the CTA ends
-        if (asked > read) warp_wait(answer, read & 1, v.err, 0x704);
+        if (asked > read) warp_wait(answer, read & 1, where, 0x704);
         if (loaded > 0) {
-            if (ok) warp_wait(q_empty, (loaded - 1) & 1, v.err, 0x301);
-            else warp_wait(q_full, (loaded - 1) & 1, v.err, 0x302);
+            if (ok) warp_wait(q_empty, (loaded - 1) & 1, where, 0x301);
+            else warp_wait(q_full, (loaded - 1) & 1, where, 0x302);
         }
         for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f) {
             const int st = f % C::STAGES;
             const uint32_t par = (f / C::STAGES) & 1;
-            if (ok) warp_wait(&kv_empty[st], par, v.err, 0x401);
-            else warp_wait(&kv_full[st], par, v.err, 0x402);
+            if (ok) warp_wait(&kv_empty[st], par, where, 0x401);
+            else warp_wait(&kv_full[st], par, where, 0x402);
         }
     } else if (warp == 9 || warp == 11) {
         // ---------------- products of row tile 0 (warp 9) and 1 (warp 11) ----------------
@@ -561,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<C::STAGES> r;   // the fill in turn
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t index) {
-                ok = ok && (mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, v.err, kWaitAttend, index));
+                ok = ok && (mbar_try_wait(bar, parity) || attend_wait(bar, parity, where, index));
             };
             auto qk = [&](int st) {   // S = Q K^T
                 const uint64_t k = dk + st * (C::TILE >> 4);
@@ -612,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // One row tile at a time from here to its next S: sharing the
                         // tensor cores, two tiles in step would stay in step, their
                         // softmaxes at once and then their products at once.
-                        ok = ok && turn_begin(const_cast<uint32_t*>(&misc[3]), v.err);
+                        ok = ok && turn_begin(const_cast<uint32_t*>(&misc[3]), where);
                         if (!ok) break;
                         tc_fence_after();
                         pv(sv, 1, false);
@@ -633,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // nothing is in flight when the CTA ends, after a wait that gave up neither
             mma_commit(drained);
-            mbar_wait_bounded(drained, 0, v.err, kWaitAttend, 0x504);
+            attend_wait(drained, 0, where, 0x504);
         }
         __syncwarp();
     } else if (warp == 10) {
@@ -643,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && items.take(w)) {
             for (int32_t x = 0; x < 2 * w.ntiles; ++x, ++fill) {
                 const int st = fill % C::STAGES;
-                ok = warp_wait(&kv_full[st], (fill / C::STAGES) & 1, v.err, 0x600);
+                ok = warp_wait(&kv_full[st], (fill / C::STAGES) & 1, where, 0x600);
                 if (!ok) break;
                 if ((x & 1) && edge_tile(w, x >> 1)) {
                     const int32_t s0 = w.lo + (x >> 1) * kKeys;
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t t0 = global_ns();
                             while (misc[1] < 8 * seen) {
                                 if (global_ns() - t0 > kWaitLimitNs) {
-                                    record_timeout(v.err, kWaitAttend, 0x601, global_ns() - t0);
+                                    *where = 0x601;
                                     ok = false;
                                     break;
                                 }
@@ -704,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) attend_record(v.err, *where);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

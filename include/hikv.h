@@ -280,8 +280,10 @@ hikv_status hikv_budgets_duo(int32_t num_layers, int32_t num_kv_heads, const uin
  * (1 .. 2e6) and records the timeout in the cache's device error word, as a
  * real stalled wait would; the kernel then returns and the context stays
  * usable.  The next hikv_device_status reports HIKV_ERR_TIMEOUT (site
- * "self-test") and clears it.  HIKV_ERR_INVALID_ARG on a null cache or a
- * limit out of range. */
+ * "self-test") and clears it.  With the environment variable
+ * HIKV_SELFTEST_SITE=9 set at the call the wait counts as one of
+ * hikv_attend_packed's (site "packed attention").  HIKV_ERR_INVALID_ARG on a
+ * null cache or a limit out of range. */
 hikv_status hikv_selftest_timeout(hikv_cache* cache, int32_t limit_us, hikv_stream_t stream);
 
 /* Number of kernels launched on the caller's streams through this cache
@@ -364,6 +366,9 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
  * out: [sum nq][Hq] rows, written; must not overlap q.  Always exact
  * attention, with an element_budget too.  May be captured as
  * hikv_append_packed.
+ * Where a bounded wait of it gives up (TIMEOUT from hikv_device_status), rows
+ * of the call may stay unwritten, and later calls write nothing before
+ * hikv_device_status has reported that.
  * Errors: INVALID_ARG (null or misaligned pointers, strides, nq < 0, rows of
  * out that overlap one another or q's), STATE
  * (more queries than the unit holds newest positions in order: the tokens it

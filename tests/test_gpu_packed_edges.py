@@ -223,3 +223,40 @@ def test_the_largest_fp32_numbers_are_numbers(hk, d, hq, hkv, where, value):
     cache.device_status()
 
 
+# ---------------------------------------------------------------------------
+# an unread time-out of the attention itself
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("f32", 64, 4, 2)])
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("held,new", [(9000, 3), (100, 3), (0, 200)])
+def test_attention_writes_nothing_while_its_timeout_is_unread(hk, dtype, d, hq, hkv, first, held, new, monkeypatch):
+    """Split over the keys or not, after another kernel's time-out (first) or alone."""
+    gen = gen_of(141)
+    cache = make(hk, 1, hq, hkv, d, dtype, 9100)
+    for n in (held, new):
+        x = rnd(gen, n, hkv, d, dtype=dtype)
+        cache.append_packed(x, rnd(gen, n, hkv, d, dtype=dtype), [n])
+    q, other = rnd(gen, new, hq, d, dtype=dtype), rnd(gen, new, hq, d, dtype=dtype)
+    out = torch.empty_like(q)
+    cache.attend_packed(other, out, [new])       # leaves its partial results in the work buffer
+    launches = cache.kernel_launches()
+    cache.attend_packed(q, out, [new])
+    assert cache.kernel_launches() - launches == 2 or held < 9000
+    check_edges(cache, q, out, [new])
+    if first:
+        cache.selftest_timeout(1000)
+    monkeypatch.setenv("HIKV_SELFTEST_SITE", "9")
+    cache.selftest_timeout(1000)
+    out.fill_(7.0)
+    cache.attend_packed(q, out, [new])
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+    with pytest.raises(hk.HikvError) as ei:
+        cache.device_status()
+    assert ei.value.status == hk.HIKV_ERR_TIMEOUT
+    assert ("self-test" if first else "packed attention") in str(ei.value)
+    cache.attend_packed(q, out, [new])
+    check_edges(cache, q, out, [new])
+    cache.device_status()
+
+
