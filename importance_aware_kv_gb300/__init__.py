@@ -455,7 +455,8 @@ class Cache:
     def attend_packed(self, q, out, nq, layer=0, stream=None):
         """Causal attention of the newest nq[b] positions of every sequence
         over everything its units hold up to them: q, out [sum nq][Hq][d]
-        (any 16-byte strides).  Append the positions' tokens first."""
+        (any 16-byte strides that keep their rows apart).  Append the
+        positions' tokens first."""
         c = self.cfg
         n, total, _keep = self._counts(nq, "nq")
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)

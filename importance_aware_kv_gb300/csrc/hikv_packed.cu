@@ -14,8 +14,9 @@ using namespace hikv;
 
 namespace {
 
-// What is wrong with packed rows, or null.  `distinct`: written rows, which
-// must not overlap one another.
+// What is wrong with packed rows, or null.  `distinct`: rows that must not
+// overlap one another -- written ones, and the queries of the attention, which
+// one tensor map describes (no stride of it may be zero).
 const char* rows_fault(const hikv_cache* c, const hikv_rows* r, int64_t total, int heads, bool distinct) {
     const int64_t e = c->esz;
     if (!r->data) return "null data";

@@ -340,7 +340,8 @@ typedef struct {
  * holds what it held at the capture (with a hikv_drop captured in front, say).
  * Errors: INVALID_ARG (null or misaligned pointers, strides, ntok < 0, a rope
  * whose table ends before the last position, q_out rows that overlap one
- * another, or q, k or v), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append). */
+ * another, or q, k or v), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append),
+ * STATE (a sequence's units at different positions).  k and v may be broadcast. */
 hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* ntok_host,
                                const hikv_rows* k, const hikv_rows* v, const hikv_rows* q,
                                const hikv_rows* q_out, const hikv_rope* rope, hikv_stream_t stream);
@@ -370,9 +371,11 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
  * of the call may stay unwritten, and later calls write nothing before
  * hikv_device_status has reported that.
  * Errors: INVALID_ARG (null or misaligned pointers, strides, nq < 0, rows of
- * out that overlap one another or q's), STATE
+ * out that overlap one another or q's, rows of q that overlap one another: a
+ * broadcast q has to be copied first), STATE
  * (more queries than the unit holds newest positions in order: the tokens it
- * holds, or those appended since its last cut). */
+ * holds, or those appended since its last cut), UNSUPPORTED (2^30 rows of q or
+ * more), OUT_OF_MEMORY (host memory). */
 hikv_status hikv_attend_packed(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const hikv_rows* q,
                                const hikv_rows* out, hikv_stream_t stream);
 

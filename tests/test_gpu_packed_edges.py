@@ -1,6 +1,6 @@
 """GPU tests of the packed-batch entry points at the edges of what they take:
 keys on both sides of every page, tile, split and causal edge, values near the
-ends of the number range, and an unread time-out.
+ends of the number range, an unread time-out, broadcast rows.
 
 Bounds on the attention's error (notation of test_gpu_packed.py: h half a step
 of the cache dtype, u = 2^-24, e the error of a logit, p the exact weights, o
@@ -257,6 +257,33 @@ def test_attention_writes_nothing_while_its_timeout_is_unread(hk, dtype, d, hq, 
     assert ("self-test" if first else "packed attention") in str(ei.value)
     cache.attend_packed(q, out, [new])
     check_edges(cache, q, out, [new])
+    cache.device_status()
+
+
+# ---------------------------------------------------------------------------
+# broadcast rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_broadcast_k_and_v_enter_and_a_broadcast_q_is_refused(hk, dtype, d):
+    gen = gen_of(161)
+    t = 70
+    cache = make(hk, 1, 8, 2, d, dtype, 200)
+    k, v = rnd(gen, t, 1, d, dtype=dtype), rnd(gen, 1, 1, d, dtype=dtype)
+    cache.append_packed(k.expand(t, 2, d), v.expand(t, 2, d), [t])
+    for g in range(2):
+        kc, vc, _ = slots(cache, g)
+        assert torch.equal(kc, k[:, 0]) and torch.equal(vc, v[:, 0].expand(t, d))
+    q = rnd(gen, t, 1, d, dtype=dtype)
+    out = torch.zeros(t, 8, d, device=DEV, dtype=DT[dtype])
+    launches = cache.kernel_launches()
+    for bad in (q.expand(t, 8, d), q[:1].expand(t, 8, d)):
+        with pytest.raises(hk.HikvError, match="q has rows that overlap") as ei:
+            cache.attend_packed(bad, out, [t])
+        assert ei.value.status == hk.HIKV_ERR_INVALID_ARG
+    assert cache.kernel_launches() == launches and not bool(out.any())
+    whole = q.expand(t, 8, d).contiguous()
+    cache.attend_packed(whole, out, [t])
+    check_edges(cache, whole, out, [t])
     cache.device_status()
 
 
