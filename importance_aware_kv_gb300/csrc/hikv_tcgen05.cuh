@@ -92,13 +92,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
         I8(r, 8), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::I8(r, 0),
-        I8(r, 8), I8(r, 16), I8(r, 24), "r"(addr)
-        : "memory");
-}
 #undef R8
 #undef RW8
 #undef I8
