@@ -85,9 +85,10 @@ struct AttendSeq {
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
 // The candidates cut the longest sequence into 1 .. 64 parts; partial results
 // must fit the work buffer.  Splitting pays where few rows see many keys:
-// five drafted tokens over eight 8K-32K caches take 122 us in three parts and
-// 316 us in one, 512 tokens over 16K 179 us in one part and 210 in seven (the
-// 238 MB of partial results cost more than even work gains).
+// five drafted tokens over eight 8K-32K caches take 311 us in one part, 163 in
+// two, 119 in three and 145 in five; two times 512 tokens over 16K 173 us in
+// one, 195 in two and 202 in three (the 34 and 51 MB of partial results cost
+// more than even work gains).
 int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* sq, int nseq, int64_t total) {
     static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
     const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = c->sm_count;

@@ -24,7 +24,7 @@
 // long as one of 128 columns would (its rows' operand, 4 KB, comes at 64 bytes a
 // cycle), so a 128 x 64 tile's S takes 3,500 cycles and its P V 1,536 of the
 // 5,800 a step; 128 keys a tile would need 544 columns of tensor memory.
-// 4096 tokens with 32/8 heads, d = 128: 695 us, 198 TFLOP/s of fp32 work (the same
+// 4096 tokens with 32/8 heads, d = 128: 698 us, 197 TFLOP/s of fp32 work (the same
 // on the CUDA cores, 4 x 4 tiles in registers: 2,947 us, 46.7).
 //
 // Non-finite V elements do not go through the products (0 x inf): they are
@@ -42,8 +42,8 @@ constexpr int kRegsSoftmax = 224, kRegsOther = 96;
 // The reference of a row's exponents in front of the maximum that it was set
 // at (a power of two), which is how far the maximum may pass before it moves:
 // weights stay below one, so that sums of finite values do not overflow
-// on the way, and the largest above 2^-16.  (4096 tokens take 688 us with 16, 710
-// with 8, 743 with 0: more rows move.  Values below 2^-94 may lose low bits.)
+// on the way, and the largest above 2^-16.  (4096 tokens took 688 us with 16, 710
+// with 8, 743 with 0 in one build: more rows move.  Values below 2^-94 may lose low bits.)
 constexpr float kAhead = 16.f;
 
 template <int D>

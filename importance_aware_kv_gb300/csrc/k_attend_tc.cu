@@ -42,7 +42,7 @@
 // 0.0023 without this; summing every rounded value gives 0.0019 too and takes
 // 358 us instead of 350.)
 //
-// Measured: 16K tokens with 64/8 heads, d = 128, 2.63 ms, 1.67 PFLOP/s; 8K with
+// Measured: 16K tokens with 64/8 heads, d = 128, 2.65 ms, 1.66 PFLOP/s; 8K with
 // 32/8 345 us, 1.59; five tokens over eight 8K-32K caches 119 us, 6.1 TB/s of
 // keys and values.  What bounds a long prompt: a row tile's step takes about
 // 2,450 cycles (softmax 770 to the first half of P, waking the issuing thread

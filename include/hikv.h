@@ -335,9 +335,15 @@ typedef struct {
  * then be NULL.  New tokens get importance 0, as by hikv_append.
  * A sequence's KV heads may hold different numbers of tokens (budgets by
  * head), but must have seen the same number of positions.
+ * A sequence may stay empty here; hikv_decode_step refuses a layer with an
+ * empty unit, hikv_score_window one with fewer positions than queries,
+ * hikv_score_band units of unequal lengths.
  * Capture: the call may be captured into a CUDA graph.  The host mirror
  * advances once, at the capture; replay the graph only where every unit of the layer
- * holds what it held at the capture (with a hikv_drop captured in front, say).
+ * holds as many tokens, up to the same position, as at the capture (with a
+ * hikv_drop captured in front, say).  Positions and lengths come from the host
+ * mirror, which sees no replay: not for a cache whose decode steps are replayed
+ * from a graph as well.
  * Errors: INVALID_ARG (null or misaligned pointers, strides, ntok < 0, a rope
  * whose table ends before the last position, q_out rows that overlap one
  * another, or q, k or v), UNSUPPORTED (rot_dim), CAPACITY (as hikv_append),
