@@ -28,11 +28,10 @@ struct hikv_cache {
     int dec_occ = 2;                    // decode CTAs per SM
     View v{};
     int32_t* d_append_base = nullptr;
-    float* d_logits = nullptr;          // long-chunk decode logits (may be null)
-    // packed attention's partial results: room for every SM's three work
-    // items of 256 query rows, or for the longest unit's keys in parts of 256
-    float* d_attend = nullptr;
-    int64_t attend_room = 0;            // floats
+    float* d_logits = nullptr;          // long-chunk decode logits; packed attention's partial results
+    // of d_logits for packed attention's partial results, in floats: every SM's
+    // three work items of 256 query rows, or the longest unit's keys in parts of 256
+    int64_t attend_room = 0;
     unsigned long long* d_cand = nullptr;
     int32_t* d_cand_slot = nullptr;
     int32_t* d_holes = nullptr;

@@ -235,8 +235,12 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
     // memory): always there (G floats a slot, 3-6 % of the K/V bytes at
     // d = 128 in bf16), so that the cluster size is chosen by cost, not by what fits
     // shared memory -- one CTA per unit with global logits beats two with
-    // shared-memory logits on ragged budgets (HeadKV workload: 157 vs 183 us)
-    const bool need_logits = true;
+    // shared-memory logits on ragged budgets (HeadKV workload: 157 vs 183 us).
+    // Packed attention's partial results live in the same buffer: no kernel of
+    // either writes it before the launches in front are complete.
+    const size_t logits = U * (size_t)c->cap * G;
+    c->attend_room = std::min<int64_t>(3LL * c->sm_count * kTcRows * (c->d + 2),
+                                       (int64_t)c->per_layer * c->cap * G * ceil_div(c->cap, 256) * (c->d + 2));
 
 #define ALLOC(ptr, n)                                                       \
     if ((e = dalloc(c, &(ptr), (n))) != cudaSuccess) {                      \
@@ -269,10 +273,7 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
     ALLOC(c->d_sassign, U + (size_t)c->L * (kSmallWarps * c->dec_occ * c->sm_count + 1));
     c->asg_key.assign(c->L, 0);
     c->sasg_key.assign(c->L, 0);
-    if (need_logits) ALLOC(c->d_logits, U * (size_t)c->cap * G);
-    c->attend_room = std::min<int64_t>(3LL * c->sm_count * kTcRows * (c->d + 2),
-                                       (int64_t)c->per_layer * c->cap * G * ceil_div(c->cap, 256) * (c->d + 2));
-    ALLOC(c->d_attend, (size_t)c->attend_room);
+    ALLOC(c->d_logits, std::max(logits, (size_t)c->attend_room));
     if (c->elem) {
         c->elem_stride = std::min(c->cap, elem_max_tokens());
         const int spans = ceil_div(c->elem_stride, elem_span_ranks());

@@ -199,8 +199,8 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.item0[a.nseq] = a.items = (int32_t)items;
         a.comb0[a.nseq] = (int32_t)split_tokens;
         a.splits = (int32_t)splits_max;
-        a.part = c->d_attend;
-        a.part_ml = c->d_attend + splits_max * a.part_rows * c->d;
+        a.part = c->d_logits;
+        a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
         cudaError_t e = bf16 ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
                              : launch_attend_f32(a, c->d, (cudaStream_t)stream);
         c->launches += 1;

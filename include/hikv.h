@@ -119,9 +119,10 @@ typedef struct {
  * on the current device.  The work buffers include the decode kernel's
  * logits for chunks too long for shared memory, G fp32 per slot of every
  * unit (max_tokens x G x 4 bytes a unit: 3 % of the K/V pool at G = 4, 6 %
- * at G = 8, with d = 128 in bf16) and hikv_attend_packed's partial results
- * (61 MB on 152 SMs at d = 128, less for caches of short units), so that no
- * call allocates.  Synchronous.
+ * at G = 8, with d = 128 in bf16), which also hold hikv_attend_packed's partial
+ * results and are enlarged for them where they are smaller than that takes (61 MB on
+ * 152 SMs at d = 128, less for caches of short units), so that no call
+ * allocates.  Synchronous.
  * On success *out owns all of it.
  * Errors: INVALID_ARG (config), UNSUPPORTED (G or d or dtype), OUT_OF_MEMORY. */
 hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out);

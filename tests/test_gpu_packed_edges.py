@@ -20,6 +20,7 @@ Norm-wise, with independent roundings of variance below h^2,
 term: n additions that each lose u of a partial sum, partial sums at most four
 times their random-walk size).
 """
+import gc
 import math
 
 import pytest
@@ -287,3 +288,38 @@ def test_broadcast_k_and_v_enter_and_a_broadcast_q_is_refused(hk, dtype, d):
     cache.device_status()
 
 
+# ---------------------------------------------------------------------------
+# memory
+# ---------------------------------------------------------------------------
+def test_large_caches_pay_no_memory_for_packed_attention(hk):
+    """Where the decode steps' logits buffer (67 MB) holds the partial results
+    of split keys (61 MB on 152 SMs), they get no memory of their own."""
+    units, cap, G, d, page = 64, 1 << 16, 4, 128, 64
+    gc.collect()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    make(hk, 1, 8, 2, d, "bf16", 256).close()      # what the first cache of a process loads
+    before = torch.cuda.mem_get_info()[0]
+    cache = make(hk, 8, 32, 8, d, "bf16", cap, page_tokens=page)
+    used = before - torch.cuda.mem_get_info()[0]
+    slots = units * cap
+    known = slots * (4 * d + 4 * G + 8) + slots // page * 8 + units * (cap // 1024) * 32 * G * 8
+    # (buffers are rounded up to 2 MB, some ten of them large)
+    assert used < known + (40 << 20), (used - known) / 2 ** 20
+    # and they serve both, in turn
+    gen = gen_of(171)
+    cache.append_packed(rnd(gen, 8 * 3000, 8, d), rnd(gen, 8 * 3000, 8, d), [3000] * 8)
+    q, q1 = rnd(gen, 8 * 5, 32, d), rnd(gen, 1, 8, 32, d)
+    out, one, other = torch.empty_like(q), torch.empty_like(q1), torch.empty_like(q1)
+    launches = cache.kernel_launches()
+    cache.attend_packed(q, out, [5] * 8)
+    assert cache.kernel_launches() == launches + 2
+    cache.decode_step(q1, one)
+    for _ in range(10):
+        again = torch.empty_like(q)
+        cache.decode_step(q1, other)
+        cache.attend_packed(q, again, [5] * 8)
+        assert torch.equal(again, out) and torch.equal(other, one)
+    check_edges(cache, q, out, [5] * 8)
+    cache.device_status()
+    cache.close()
