@@ -24,7 +24,7 @@
 // long as one of 128 columns would (its rows' operand, 4 KB, comes at 64 bytes a
 // cycle), so a 128 x 64 tile's S takes 3,500 cycles and its P V 1,536 of the
 // 5,800 a step; 128 keys a tile would need 544 columns of tensor memory.
-// 4096 tokens with 32/8 heads, d = 128: 698 us, 197 TFLOP/s of fp32 work (the same
+// 4096 tokens with 32/8 heads, d = 128: 690 us, 199 TFLOP/s of fp32 work (the same
 // on the CUDA cores, 4 x 4 tiles in registers: 2,947 us, 46.7).
 //
 // Non-finite V elements do not go through the products (0 x inf): they are
@@ -39,12 +39,12 @@ constexpr int kThreads = 512, kConvert = 256;
 constexpr int kRows = kF32Rows, kKeys = kF32Keys;
 // 128 x 224 + 384 x 96 registers = the 512 x 128 at launch
 constexpr int kRegsSoftmax = 224, kRegsOther = 96;
-// The reference of a row's exponents in front of the maximum that it was set
-// at (a power of two), which is how far the maximum may pass before it moves:
-// weights stay below one, so that sums of finite values do not overflow
-// on the way, and the largest above 2^-16.  (4096 tokens took 688 us with 16, 710
-// with 8, 743 with 0 in one build: more rows move.  Values below 2^-94 may lose low bits.)
-constexpr float kAhead = 16.f;
+// How far the maximum may pass the one that a row's exponents refer to before the
+// reference moves, in powers of two, and the factor that keeps the weights at one
+// or below till then, so that sums of finite values do not overflow on the way;
+// the largest weight is above 2^-16.  (4096 tokens took 688 us with 16, 710 with
+// 8, 743 with 0 in one build: more rows move.  Values below 2^-94 may lose low bits.)
+constexpr float kAhead = 16.f, kWeight = 1.f / 65536.f;
 
 template <int D>
 struct F3 {
@@ -218,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             if (lane == 0) mbar_arrive(q_full);
         }
         float m = -INFINITY, l = 0.f;   // m: the maximum at the reference's last move
-        auto reference = [&] { return m == -INFINITY ? 0.f : fmaf(m, c, kAhead); };
         float2 acc[D / 2];
 #pragma unroll
         for (int j = 0; j < D / 2; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -268,13 +267,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             const bool move = (mt - m) * c > kAhead;
             const float f = move ? ex2((m - mt) * c) : 1.f;
             if (move) m = mt;
-            const float base = reference();
+            const float base = m == -INFINITY ? 0.f : m * c;
             const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
-                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                // (2^-kAhead as a factor: in the exponent it would cost the low bits of small ones)
+                const float2 e = ffma2(make_float2(ex2(x.x), ex2(x.y)), make_float2(kWeight, kWeight), make_float2(0.f, 0.f));
                 sum = fadd2(sum, e);
                 s[2 * j] = __float_as_uint(e.x);
                 s[2 * j + 1] = __float_as_uint(e.y);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             if (splits > 1 && row < rows) {
                 const int32_t tok = first + (row >> a.gshift), h = (g << a.gshift) + (row & ((1 << a.gshift) - 1));
                 const int64_t pr = (int64_t)split * a.part_rows + (int64_t)tok * v.hq + h;
-                *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m == -INFINITY ? m : reference(), l);
+                *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
             }
         }
     } else {
