@@ -368,8 +368,8 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
  * round the probabilities to bf16 for the product with V, fp32 caches form
  * every product to 2^-22 of it.  Weights are at most one in these sums, so
  * that finite values do not overflow while n max |v| is finite; values below
- * 2^-94 (bf16: 2^-102) may lose low bits.  A K or V row that a query does not see does
- * not touch its output, whatever it holds.  (fp32: a non-finite element of
+ * 2^-94 (bf16: 2^-102) may lose bits or vanish.  A K or V row that a query does
+ * not see does not touch its output, whatever it holds.  (fp32: a non-finite element of
  * q, or of a k that is seen, makes the row NaN.)
  * out: [sum nq][Hq] rows, written; must not overlap q.  Always exact
  * attention, with an element_budget too.  May be captured as
