@@ -318,7 +318,7 @@ def prepare(case, seed):
         s["case"] = case
         units = case["layers"] * batch * hkv
         if own:
-            z = torch.zeros(1, 1, 1, device="cuda", dtype=dt).expand(sum(held), hkv, d)
+            z = torch.zeros(1, 1, d, device="cuda", dtype=dt).expand(sum(held), hkv, d)
             for layer in range(case["layers"]):
                 cache.append_packed(z, z, held, layer=layer)
             view = cache.device_view()
