@@ -34,7 +34,8 @@ ABI_FUNCTIONS = ("hikv_create_cache", "hikv_destroy_cache", "hikv_append", "hikv
                  "hikv_budgets_duo", "hikv_selftest_timeout", "hikv_element_rows",
                  "hikv_last_decode_config", "hikv_score_band", "hikv_read_floor",
                  "hikv_read_slot", "hikv_append_packed", "hikv_attend_packed", "hikv_drop",
-                 "hikv_device_view")
+                 "hikv_device_view", "hikv_attend_window", "hikv_tree_masks", "hikv_append_tree",
+                 "hikv_attend_tree", "hikv_accept", "hikv_fork")
 
 
 class HikvError(RuntimeError):
@@ -102,6 +103,12 @@ def _load():
         "hikv_attend_packed": ([P, I32] + [P] * 4, S),
         "hikv_drop": ([P, I32, I32, P, P], S),
         "hikv_device_view": ([P, ctypes.POINTER(hikv_view)], S),
+        "hikv_attend_window": ([P, I32, P, P, I32, P, P, P], S),
+        "hikv_tree_masks": ([P, P, P, P, I32, P, P], S),
+        "hikv_append_tree": ([P, I32] + [P] * 8, S),
+        "hikv_attend_tree": ([P, I32, P, P, I32, P, P, P], S),
+        "hikv_accept": ([P, I32, I32, P, P, P, P], S),
+        "hikv_fork": ([P, I32, I32, P, P, P], S),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -193,6 +200,26 @@ class Rope:
         self.device_index = cos.device.index
         self.c = hikv_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
         self.ref = ctypes.byref(self.c)
+
+
+class Tree:
+    """What the nodes of a batch of drafted trees see, for Cache.attend_tree and
+    Cache.append_tree: ntok[b] nodes of sequence b, mask [sum ntok][words] int32
+    (bit j % 32 of word j / 32: the node sees node j of its sequence), depth
+    [sum ntok] int32 (append_tree only).  Cache.tree makes one from parents; masks
+    of any shape can be given here.  Keeps the tensors alive."""
+
+    def __init__(self, ntok, mask, depth=None):
+        import torch
+        _dev(mask, "mask", torch.int32)
+        if mask.dim() != 2:
+            raise ValueError(f"mask has shape {tuple(mask.shape)}, expected [nodes][words]")
+        if depth is not None:
+            _dev(depth, "depth", torch.int32, mask.shape[:1])
+            if depth.device != mask.device:
+                raise ValueError("mask and depth are on different devices")
+        self.ntok, self.mask, self.depth = ntok, mask, depth
+        self.device_index = mask.device.index
 
 
 class _DeviceArray:
@@ -461,6 +488,114 @@ class Cache:
         n, total, _keep = self._counts(nq, "nq")
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
         _check(_lib.hikv_attend_packed(self.h, layer, n, rq, ro, self._stream_int(stream)))
+
+    def attend_window(self, q, out, nq, window, sink=0, layer=0, stream=None):
+        """attend_packed with a sliding window: a query sees the newest
+        window[g] positions up to its own (a number, or one for every KV head;
+        0: all) and the first sink positions."""
+        c = self.cfg
+        n, total, _keep = self._counts(nq, "nq")
+        if isinstance(window, (int, np.integer)) and not isinstance(window, bool):
+            window = [window] * c.num_kv_heads
+        w = self._ints(window, "window", c.num_kv_heads)
+        rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
+        _check(_lib.hikv_attend_window(self.h, layer, n, w.buffer_info()[0], int(sink), rq, ro,
+                                       self._stream_int(stream)))
+
+    def tree(self, parent, ntok, stream=None):
+        """The masks and depths of a batch of drafted trees: parent [sum ntok]
+        int32 on the cache's device, each node's parent in its own sequence (an
+        earlier node), -1 for a child of the last token before the tree."""
+        import torch
+        n, total, keep = self._counts(ntok, "ntok")
+        _dev(parent, "parent", torch.int32, (total,))
+        if parent.get_device() != self.device_index:
+            raise ValueError(f"parent is on {parent.device}, the cache on cuda:{self.device_index}")
+        words = max(1, -(-int(max(keep)) // 32))
+        s = self._stream_int(stream)
+        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device=parent.device)):
+            mask = torch.empty(total, words, dtype=torch.int32, device=parent.device)
+            depth = torch.empty(total, dtype=torch.int32, device=parent.device)
+        _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
+        return Tree(ntok, mask, depth)
+
+    def _tree(self, tree, total, name):
+        """A Tree's tensors checked against the packed rows of a call."""
+        if tree.device_index != self.device_index:
+            raise ValueError(f"the tree is on {tree.mask.device}, the cache on cuda:{self.device_index}")
+        t = getattr(tree, name)
+        if t is None:
+            raise ValueError(f"the tree has no {name}")
+        if t.shape[0] != total:
+            raise ValueError(f"{name} has {t.shape[0]} rows, the tree {total} nodes")
+        return t.data_ptr()
+
+    def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):
+        """append_packed of a Tree's nodes, k (and q) rotated by the position of
+        the sequence's first node plus the node's depth."""
+        c = self.cfg
+        n, total, _keep = self._counts(tree.ntok, "ntok")
+        depth = self._tree(tree, total, "depth")
+        rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        rq = ro = None
+        if q is not None:
+            rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, q_out, "q_out", total, c.num_q_heads)
+        if rope.device_index != self.device_index:
+            raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
+        _check(_lib.hikv_append_tree(self.h, layer, n, depth, rk, rv, rq, ro, rope.ref, self._stream_int(stream)))
+
+    def attend_tree(self, q, out, tree, layer=0, stream=None):
+        """Attention of the newest tree.ntok[b] tokens of every sequence over
+        everything in front of them and, among themselves, what the tree's masks
+        say: q, out [sum ntok][Hq][d] as for attend_packed."""
+        c = self.cfg
+        n, total, _keep = self._counts(tree.ntok, "ntok")
+        mask = self._tree(tree, total, "mask")
+        rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
+        _check(_lib.hikv_attend_tree(self.h, layer, n, mask, tree.mask.shape[1], rq, ro, self._stream_int(stream)))
+
+    def accept(self, ntree, accepted, layer0=0, nlayers=None, stream=None):
+        """Keep, of the newest ntree[b] tokens of batch row b, those that the
+        list accepted[b] names (0 .. ntree[b] - 1, ascending), drop the others.
+        ntree: counts, or the Tree."""
+        n, _, _keep = self._counts(ntree.ntok if isinstance(ntree, Tree) else ntree, "ntree")
+        if len(accepted) != self.cfg.batch:
+            raise ValueError(f"accepted has {len(accepted)} lists, expected {self.cfg.batch}")
+        lists = [x if type(x) is list else list(x) for x in accepted]
+        counts = self._ints([len(x) for x in lists], "accepted", self.cfg.batch)
+        flat = [i for x in lists for i in x]
+        index = self._ints(flat, "accepted", len(flat))
+        nl = self.cfg.num_layers - layer0 if nlayers is None else nlayers
+        _check(_lib.hikv_accept(self.h, layer0, nl, n, counts.buffer_info()[0], index.buffer_info()[0],
+                                self._stream_int(stream)))
+
+    def fork(self, src, same=None, layer0=0, nlayers=None, stream=None):
+        """Batch row b becomes a copy of row src[b] (b or -1: it stays).  The
+        first same[b] slots, promised to be equal already, are not copied."""
+        s = self._ints(src, "src", self.cfg.batch)
+        m = None if same is None else self._ints(same, "same", self.cfg.batch)
+        nl = self.cfg.num_layers - layer0 if nlayers is None else nlayers
+        _check(_lib.hikv_fork(self.h, layer0, nl, s.buffer_info()[0], None if m is None else m.buffer_info()[0],
+                              self._stream_int(stream)))
+
+    @staticmethod
+    def _ints(values, name, count):
+        """HOST int32 [count] from a list, array or CPU tensor of whole numbers."""
+        if type(values) not in (list, tuple) or not set(map(type, values)) <= {int}:
+            a = np.asarray(values)
+            if a.size and a.dtype.kind not in "iu":
+                raise TypeError(f"{name} must hold whole numbers")
+            if a.ndim != 1:
+                raise ValueError(f"{name} has shape {a.shape}, expected ({count},)")
+            values = a.tolist()
+        if len(values) != count:
+            raise ValueError(f"{name} has {len(values)} values, expected {count}")
+        try:
+            return array.array("i", values)
+        except OverflowError:
+            raise ValueError(f"{name} holds values out of range") from None
 
     def drop(self, counts=None, layer0=0, nlayers=None, stream=None):
         """Drop the newest counts[b] tokens of every unit of batch row b (-1,

@@ -5,6 +5,7 @@
 #include <climits>
 #include <cstdint>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "hikv_cache.cuh"
@@ -75,12 +76,40 @@ struct ItemShape {
 constexpr ItemShape kTcShape{kTcRows, kTcKeys, 2.0, 3.0, 7.5e6};
 constexpr ItemShape kF32Shape{kF32Rows, kF32Keys, 1.5, 1.5, 15e6};
 
+// What the queries of a call see (hikv_packed.cuh), and the KV heads by window.
+struct Sees {
+    int kind = CausalMask::kind;
+    WindowMask window{};
+    TreeMask tree{};
+    std::vector<std::pair<int32_t, int>> heads;   // window length, KV heads
+};
+
 // A sequence of a call: its batch row, first packed row, queries, and the
 // longest and the mean length of its heads, and whether all are as long.
 struct AttendSeq {
     int32_t brow, start, nq, n, mean;
     bool equal;
 };
+
+// Keys of the work items of row tile t of a sequence, for heads of one window
+int64_t item_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq& s, int64_t t, int32_t window) {
+    if (sees.kind == TreeMask::kind) return s.n;
+    const int64_t seen = s.n - s.nq + std::min<int64_t>(s.nq, (t + 1) * k.rows / c->G);
+    if (sees.kind == CausalMask::kind) return seen;
+    const int64_t align = sees.window.align, gap = (sees.window.sink + align - 1) / align * align;
+    const int64_t start = std::max<int64_t>(s.n - s.nq + t * k.rows / c->G - window + 1, 0) / align * align;
+    return seen - std::max<int64_t>(start - gap, 0);
+}
+// the most keys of a work item of a sequence
+int64_t most_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq& s) {
+    if (sees.kind != WindowMask::kind) return s.n;
+    const int64_t tiles = ((int64_t)s.nq * c->G + k.rows - 1) / k.rows;
+    int64_t most = 0;
+    for (const auto& h : sees.heads)   // the last tiles span most keys; the last but one may have more rows
+        for (int64_t t = std::max<int64_t>(0, tiles - 2); t < tiles; ++t)
+            most = std::max(most, item_keys(c, k, sees, s, t, h.first));
+    return std::min<int64_t>(most + sees.window.align, s.n);   // (windows of inner tiles may start lower in a box)
+}
 
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
 // The candidates cut the longest sequence into 1 .. 64 parts; partial results
@@ -89,12 +118,15 @@ struct AttendSeq {
 // two, 119 in three and 145 in five; two times 512 tokens over 16K 173 us in
 // one, 195 in two and 202 in three (the 34 and 51 MB of partial results cost
 // more than even work gains).
-int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* sq, int nseq, int64_t total) {
+int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq* sq, int nseq,
+                     int64_t total) {
     static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
-    const int64_t maxsteps = ceil_div(sq[0].n, k.keys), slots = c->sm_count;
-    int64_t base_items = 0;
+    const int64_t slots = c->sm_count;
+    int64_t base_items = 0, most = 0;
     for (int i = 0; i < nseq; ++i) base_items += (((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows) * c->Hkv;
     if (base_items >= 4 * slots) return INT32_MAX;
+    for (int i = 0; i < nseq; ++i) most = std::max(most, most_keys(c, k, sees, sq[i]));
+    const int64_t maxsteps = (most + k.keys - 1) / k.keys;
     double best = 0;
     int32_t best_chunk = INT32_MAX;
     int64_t last = 0;
@@ -110,13 +142,13 @@ int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* s
         for (int i = 0; i < nseq; ++i) {
             const int64_t tiles = ((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows;
             const double share = (double)sq[i].mean / sq[i].n;
-            for (int64_t t = 0; t < tiles; ++t) {
-                const int64_t seen = sq[i].n - sq[i].nq + std::min<int64_t>(sq[i].nq, (t + 1) * k.rows / c->G);
-                const int64_t st = (seen + k.keys - 1) / k.keys;
-                items += (st + ct - 1) / ct * c->Hkv;
-                steps += share * st * c->Hkv;
-                longest = std::max(longest, (double)std::min(st, ct));
-            }
+            for (int64_t t = 0; t < tiles; ++t)
+                for (const auto& h : sees.heads) {
+                    const int64_t st = (item_keys(c, k, sees, sq[i], t, h.first) + k.keys - 1) / k.keys;
+                    items += (st + ct - 1) / ct * h.second;
+                    steps += share * st * h.second;
+                    longest = std::max(longest, (double)std::min(st, ct));
+                }
         }
         double cost = std::max((steps + items * k.item_steps) / slots, longest + k.item_steps);
         if (items > slots) cost += 0.5 * longest;
@@ -129,13 +161,31 @@ int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const AttendSeq* s
     return best_chunk;
 }
 
-// The launches of hikv_attend_packed, its arguments checked.
+cudaError_t launch_kernels(const hikv_cache* c, const Sees& sees, const AttendArgs& a, const CUtensorMap& qmap, cudaStream_t s) {
+    const bool bf16 = c->dtype == HIKV_BF16;
+    if (sees.kind == WindowMask::kind)
+        return bf16 ? launch_attend_tc_window(a, sees.window, qmap, c->tmap_page, c->d, s)
+                    : launch_attend_f32_window(a, sees.window, c->d, s);
+    if (sees.kind == TreeMask::kind)
+        return bf16 ? launch_attend_tc_tree(a, sees.tree, qmap, c->tmap_page, c->d, s)
+                    : launch_attend_f32_tree(a, sees.tree, c->d, s);
+    return bf16 ? launch_attend_tc(a, qmap, c->tmap_page, c->d, s) : launch_attend_f32(a, c->d, s);
+}
+cudaError_t launch_join(const hikv_cache* c, const Sees& sees, const AttendArgs& a, cudaStream_t s) {
+    if (sees.kind == WindowMask::kind) return launch_attend_join_window(a, sees.window, c->dtype, c->d, s);
+    if (sees.kind == TreeMask::kind) return launch_attend_join_tree(a, sees.tree, c->dtype, c->d, s);
+    return launch_attend_join(a, c->dtype, c->d, s);
+}
+
+// The launches of the packed attention calls, their arguments checked.
 hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t total, const hikv_rows* q,
-                          const hikv_rows* out, hikv_stream_t stream) {
+                          const hikv_rows* out, Sees& sees, hikv_stream_t stream, const char* who) {
     DeviceGuard guard(c->device);
-    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "attend_packed: device");
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who);
     pdl_forget(c);
     const bool bf16 = c->dtype == HIKV_BF16;
+    sees.window.align = bf16 ? std::min(c->P, 128) : 1;   // rows of a box of the tensor map of the pages
+    if (sees.kind != WindowMask::kind) sees.heads.assign(1, {kAllSlots, c->Hkv});
     CUtensorMap qmap;
     if (bf16) {
         // q as [tokens][heads][d], boxes of 128 query rows x 128 bytes
@@ -148,7 +198,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: no tensor map of q (%d)", (int)r);
+        if (r != CUDA_SUCCESS) return fail(HIKV_ERR_INVALID_ARG, "%s: no tensor map of q (%d)", who, (int)r);
     }
     AttendArgs a{};
     a.v = c->v;
@@ -179,11 +229,11 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
     for (size_t s0 = 0; s0 < seqs.size(); s0 += kAttSeqs) {
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const AttendSeq* sq = seqs.data() + s0;
-        a.chunk = attend_chunk(c, shape, sq, a.nseq, total);
+        a.chunk = attend_chunk(c, shape, sees, sq, a.nseq, total);
         int64_t items = 0, split_tokens = 0, splits_max = 0;
         for (int i = 0; i < a.nseq; ++i) {
             const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;
-            const int64_t splits = ((int64_t)sq[i].n + a.chunk - 1) / a.chunk;
+            const int64_t splits = (most_keys(c, shape, sees, sq[i]) + a.chunk - 1) / a.chunk;
             a.brow[i] = sq[i].brow;
             a.start[i] = sq[i].start;
             a.nq[i] = sq[i].nq;
@@ -195,61 +245,95 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             split_tokens += splits > 1 ? sq[i].nq : 0;
             splits_max = std::max(splits_max, splits);
         }
-        if (items > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
+        if (items > INT32_MAX) return fail(HIKV_ERR_UNSUPPORTED, "%s: too many queries in one call", who);
         a.item0[a.nseq] = a.items = (int32_t)items;
         a.comb0[a.nseq] = (int32_t)split_tokens;
         a.splits = (int32_t)splits_max;
         a.part = c->d_logits;
         a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
-        cudaError_t e = bf16 ? launch_attend_tc(a, qmap, c->tmap_page, c->d, (cudaStream_t)stream)
-                             : launch_attend_f32(a, c->d, (cudaStream_t)stream);
+        cudaError_t e = launch_kernels(c, sees, a, qmap, (cudaStream_t)stream);
         c->launches += 1;
         if (e == cudaSuccess && split_tokens > 0) {
-            e = launch_attend_join(a, c->dtype, c->d, (cudaStream_t)stream);
+            e = launch_join(c, sees, a, (cudaStream_t)stream);
             c->launches += 1;
         }
-        if (e != cudaSuccess) return cuda_fail(e, "attend_packed: launch");
+        if (e != cudaSuccess) return cuda_fail(e, who);
     }
     return HIKV_OK;
+}
+
+// The checks that the packed attention calls share; *total = 0: nothing to do
+hikv_status attend_check(const hikv_cache* c, int32_t layer, const int32_t* nq, const hikv_rows* q, const hikv_rows* out,
+                         int64_t* total, const char* who) {
+    *total = 0;
+    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "%s: bad cache or layer", who);
+    if (!nq || !q || !out) return fail(HIKV_ERR_INVALID_ARG, "%s: null nq, q or out", who);
+    const int64_t n = packed_total(c, nq);
+    if (n < 0) return fail(HIKV_ERR_INVALID_ARG, "%s: a query count is negative or their sum too large", who);
+    if (n == 0) return HIKV_OK;
+    if (n * c->Hq > INT32_MAX / 2) return fail(HIKV_ERR_UNSUPPORTED, "%s: too many queries in one call", who);
+    const char* bad = nullptr;
+    if ((bad = rows_fault(c, q, n, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "%s: q has %s", who, bad);
+    if ((bad = rows_fault(c, out, n, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "%s: out has %s", who, bad);
+    if (rows_meet(c, out, c->Hq, q, c->Hq, n)) return fail(HIKV_ERR_INVALID_ARG, "%s: out overlaps q", who);
+    const int u0 = layer * c->per_layer;
+    for (int i = 0; i < c->per_layer; ++i)
+        if (nq[i / c->Hkv] > c->tail[u0 + i])
+            return fail(HIKV_ERR_STATE, "%s: %d queries of unit %d, which holds its newest %d in order", who,
+                        nq[i / c->Hkv], u0 + i, c->tail[u0 + i]);
+    *total = n;
+    return HIKV_OK;
+}
+
+// attend_launch for a C caller
+hikv_status attend_call(hikv_cache* c, int32_t layer, const int32_t* nq, int64_t total, const hikv_rows* q,
+                        const hikv_rows* out, Sees& sees, hikv_stream_t stream, const char* who) {
+    try {
+        return attend_launch(c, layer * c->per_layer, nq, total, q, out, sees, stream, who);
+    } catch (const std::bad_alloc&) {
+        return fail(HIKV_ERR_OUT_OF_MEMORY, "%s: host memory", who);
+    }
 }
 
 }  // namespace
 
 extern "C" {
 
-hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok, const hikv_rows* k,
-                               const hikv_rows* vv, const hikv_rows* q, const hikv_rows* q_out,
-                               const hikv_rope* rope, hikv_stream_t stream) {
-    set_last_error("");
-    NvtxRange nvtx("hikv_append_packed");
-    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "append_packed: bad cache or layer");
-    if (!ntok || !k || !vv) return fail(HIKV_ERR_INVALID_ARG, "append_packed: null ntok, k or v");
+namespace {
+// hikv_append_packed, and (tree) hikv_append_tree
+hikv_status append_rows(hikv_cache* c, int32_t layer, const int32_t* ntok, bool tree, const int32_t* depth, const hikv_rows* k,
+                        const hikv_rows* vv, const hikv_rows* q, const hikv_rows* q_out, const hikv_rope* rope,
+                        hikv_stream_t stream, const char* who) {
+    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "%s: bad cache or layer", who);
+    if (!ntok || !k || !vv) return fail(HIKV_ERR_INVALID_ARG, "%s: null ntok, k or v", who);
     const int64_t total = packed_total(c, ntok);
-    if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "append_packed: a token count is negative or their sum too large");
+    if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "%s: a token count is negative or their sum too large", who);
     if (total == 0) return HIKV_OK;
     if ((q != nullptr) != (q_out != nullptr))
-        return fail(HIKV_ERR_INVALID_ARG, "append_packed: q and q_out go together");
-    if (q && !rope) return fail(HIKV_ERR_INVALID_ARG, "append_packed: q without a rope");
+        return fail(HIKV_ERR_INVALID_ARG, "%s: q and q_out go together", who);
+    if (q && !rope) return fail(HIKV_ERR_INVALID_ARG, "%s: q without a rope", who);
+    if (tree && (!depth || ((uintptr_t)depth & 3) || !rope))
+        return fail(HIKV_ERR_INVALID_ARG, "%s: null or misaligned depth, or no rope", who);
     const char* bad = nullptr;
-    if ((bad = rows_fault(c, k, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: k has %s", bad);
-    if ((bad = rows_fault(c, vv, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: v has %s", bad);
+    if ((bad = rows_fault(c, k, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "%s: k has %s", who, bad);
+    if ((bad = rows_fault(c, vv, total, c->Hkv, false))) return fail(HIKV_ERR_INVALID_ARG, "%s: v has %s", who, bad);
     if (q) {
-        if ((bad = rows_fault(c, q, total, c->Hq, false))) return fail(HIKV_ERR_INVALID_ARG, "append_packed: q has %s", bad);
+        if ((bad = rows_fault(c, q, total, c->Hq, false))) return fail(HIKV_ERR_INVALID_ARG, "%s: q has %s", who, bad);
         if ((bad = rows_fault(c, q_out, total, c->Hq, true)))
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out has %s", bad);
+            return fail(HIKV_ERR_INVALID_ARG, "%s: q_out has %s", who, bad);
         if (q->data == q_out->data && (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out in the place of q needs its strides");
+            return fail(HIKV_ERR_INVALID_ARG, "%s: q_out in the place of q needs its strides", who);
         if ((q->data != q_out->data && rows_meet(c, q_out, c->Hq, q, c->Hq, total)) ||
             rows_meet(c, q_out, c->Hq, k, c->Hkv, total) || rows_meet(c, q_out, c->Hq, vv, c->Hkv, total))
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: q_out overlaps q, k or v");
+            return fail(HIKV_ERR_INVALID_ARG, "%s: q_out overlaps q, k or v", who);
     }
     if (rope) {
         if (!rope->cos || !rope->sin || (((uintptr_t)rope->cos | (uintptr_t)rope->sin) & 15))
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: null or misaligned rope tables");
+            return fail(HIKV_ERR_INVALID_ARG, "%s: null or misaligned rope tables", who);
         if (rope->interleaved != 0 && rope->interleaved != 1)
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: interleaved %d not in {0, 1}", rope->interleaved);
+            return fail(HIKV_ERR_INVALID_ARG, "%s: interleaved %d not in {0, 1}", who, rope->interleaved);
         if (rope->rot_dim < 16 || rope->rot_dim > c->d || rope->rot_dim % 16)
-            return fail(HIKV_ERR_UNSUPPORTED, "append_packed: rot_dim %d is no multiple of 16 up to head_dim %d",
+            return fail(HIKV_ERR_UNSUPPORTED, "%s: rot_dim %d is no multiple of 16 up to head_dim %d", who,
                         rope->rot_dim, c->d);
     }
     const int u0 = layer * c->per_layer, Hkv = c->Hkv;
@@ -261,23 +345,23 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         const int32_t *len = c->len.data() + ub, *mapped = c->mapped.data() + ub, *next_pos = c->next_pos.data() + ub;
         for (int g = 0; g < Hkv; ++g) {
             if ((int64_t)len[g] + m > c->cap)
-                return fail(HIKV_ERR_CAPACITY, "append_packed: unit %d would hold %lld > max_tokens %d", ub + g,
+                return fail(HIKV_ERR_CAPACITY, "%s: unit %d would hold %lld > max_tokens %d", who, ub + g,
                             (long long)len[g] + m, c->cap);
             if (next_pos[g] != next_pos[0])
-                return fail(HIKV_ERR_STATE, "append_packed: units %d and %d are at different positions", ub + g, ub);
+                return fail(HIKV_ERR_STATE, "%s: units %d and %d are at different positions", who, ub + g, ub);
             new_pages += std::max(0, ((len[g] + m - 1) >> c->page_shift) + 1 - mapped[g]);
         }
         const int64_t end = (int64_t)next_pos[0] + m;
-        if (end > INT32_MAX) return fail(HIKV_ERR_CAPACITY, "append_packed: positions of batch row %d overflow int32", b);
+        if (end > INT32_MAX) return fail(HIKV_ERR_CAPACITY, "%s: positions of batch row %d overflow int32", who, b);
         if (rope && end > rope->positions)
-            return fail(HIKV_ERR_INVALID_ARG, "append_packed: batch row %d reaches position %lld, the rope has %d", b,
+            return fail(HIKV_ERR_INVALID_ARG, "%s: batch row %d reaches position %lld, the rope has %d", who, b,
                         (long long)end - 1, rope->positions);
     }
     if (c->pages_in_use + new_pages > c->pool_pages)
-        return fail(HIKV_ERR_CAPACITY, "append_packed: page pool exhausted (%lld in use + %lld > %lld)",
+        return fail(HIKV_ERR_CAPACITY, "%s: page pool exhausted (%lld in use + %lld > %lld)", who,
                     (long long)c->pages_in_use, (long long)new_pages, (long long)c->pool_pages);
     DeviceGuard guard(c->device);
-    if (guard.status != cudaSuccess) return cuda_fail(guard.status, "append_packed: device");
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who);
     pdl_forget(c);
     PackedAppendArgs a{};
     a.v = c->v;
@@ -293,6 +377,7 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         a.sin = rope->sin;
         a.rot = rope->rot_dim;
         a.interleaved = rope->interleaved;
+        a.depth = depth;
     }
     int32_t row = 0;
     for (int b0 = 0; b0 < c->B; b0 += kSeqMax) {
@@ -318,7 +403,7 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
         a.reserved = known ? nullptr : c->d_append_base;
         cudaError_t e = launch_append_packed(a, c->dtype, c->sm_count, (cudaStream_t)stream);
         c->launches += known ? 1 : 2;
-        if (e != cudaSuccess) return cuda_fail(e, "append_packed: launch");
+        if (e != cudaSuccess) return cuda_fail(e, who);
         for (int i = 0; i < n; ++i) {
             const int m = ntok[b0 + i], ub = u0 + (b0 + i) * Hkv;
             if (m == 0) continue;
@@ -338,30 +423,95 @@ hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok
     return HIKV_OK;
 }
 
+}  // namespace
+
+hikv_status hikv_append_packed(hikv_cache* c, int32_t layer, const int32_t* ntok, const hikv_rows* k,
+                               const hikv_rows* vv, const hikv_rows* q, const hikv_rows* q_out,
+                               const hikv_rope* rope, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_append_packed");
+    return append_rows(c, layer, ntok, false, nullptr, k, vv, q, q_out, rope, stream, "append_packed");
+}
+
+hikv_status hikv_append_tree(hikv_cache* c, int32_t layer, const int32_t* ntok, const int32_t* depth,
+                             const hikv_rows* k, const hikv_rows* vv, const hikv_rows* q, const hikv_rows* q_out,
+                             const hikv_rope* rope, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_append_tree");
+    return append_rows(c, layer, ntok, true, depth, k, vv, q, q_out, rope, stream, "append_tree");
+}
+
 hikv_status hikv_attend_packed(hikv_cache* c, int32_t layer, const int32_t* nq, const hikv_rows* q,
                                const hikv_rows* out, hikv_stream_t stream) {
     set_last_error("");
     NvtxRange nvtx("hikv_attend_packed");
-    if (!range_ok(c, layer, 1)) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: bad cache or layer");
-    if (!nq || !q || !out) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: null nq, q or out");
-    const int64_t total = packed_total(c, nq);
-    if (total < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: a query count is negative or their sum too large");
+    int64_t total;
+    const hikv_status st = attend_check(c, layer, nq, q, out, &total, "attend_packed");
+    if (st != HIKV_OK || total == 0) return st;
+    Sees sees;
+    return attend_call(c, layer, nq, total, q, out, sees, stream, "attend_packed");
+}
+
+hikv_status hikv_attend_window(hikv_cache* c, int32_t layer, const int32_t* nq, const int32_t* window, int32_t sink,
+                               const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_attend_window");
+    int64_t total;
+    const hikv_status st = attend_check(c, layer, nq, q, out, &total, "attend_window");
+    if (st != HIKV_OK) return st;
+    if (!window || sink < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_window: null window or negative sink");
+    for (int g = 0; g < c->Hkv; ++g)
+        if (window[g] < 0) return fail(HIKV_ERR_INVALID_ARG, "attend_window: window[%d]=%d is negative", g, window[g]);
+    if (c->Hkv > kAttHeads)
+        return fail(HIKV_ERR_UNSUPPORTED, "attend_window: %d KV heads, more than %d", c->Hkv, kAttHeads);
     if (total == 0) return HIKV_OK;
-    if (total * c->Hq > INT32_MAX / 2) return fail(HIKV_ERR_UNSUPPORTED, "attend_packed: too many queries in one call");
-    const char* bad = nullptr;
-    if ((bad = rows_fault(c, q, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: q has %s", bad);
-    if ((bad = rows_fault(c, out, total, c->Hq, true))) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out has %s", bad);
-    if (rows_meet(c, out, c->Hq, q, c->Hq, total)) return fail(HIKV_ERR_INVALID_ARG, "attend_packed: out overlaps q");
     const int u0 = layer * c->per_layer;
-    for (int i = 0; i < c->per_layer; ++i)
-        if (nq[i / c->Hkv] > c->tail[u0 + i])
-            return fail(HIKV_ERR_STATE, "attend_packed: %d queries of unit %d, which holds its newest %d in order",
-                        nq[i / c->Hkv], u0 + i, c->tail[u0 + i]);
-    try {
-        return attend_launch(c, u0, nq, total, q, out, stream);
-    } catch (const std::bad_alloc&) {
-        return fail(HIKV_ERR_OUT_OF_MEMORY, "attend_packed: host memory");
+    int longest = 0;
+    for (int i = 0; i < c->per_layer; ++i) {
+        const int u = u0 + i, n = nq[i / c->Hkv], w = window[i % c->Hkv];
+        if (n == 0) continue;
+        longest = std::max(longest, c->len[u]);
+        // a cut moves survivors: the window has to lie in what was appended since, the first tokens where they stay
+        if (w > 0 && c->tail[u] < c->len[u] && (c->tail[u] < (int64_t)n + w - 1 || sink > c->S))
+            return fail(HIKV_ERR_STATE,
+                        "attend_window: unit %d was cut and holds its newest %d in order, %d queries with a window of %d "
+                        "need %lld, and at most %d first tokens", u, c->tail[u], n, w, (long long)n + w - 1, c->S);
     }
+    Sees sees;
+    sees.window.sink = std::min(sink, c->cap);
+    bool hides = false;
+    try {
+        for (int g = 0; g < c->Hkv; ++g) {
+            // (a window that reaches the first tokens hides nothing)
+            const int32_t w = window[g] == 0 || (int64_t)window[g] + sink >= longest ? kAllSlots : window[g];
+            sees.window.window[g] = w;
+            hides |= w != kAllSlots;
+            auto h = std::find_if(sees.heads.begin(), sees.heads.end(), [&](const auto& x) { return x.first == w; });
+            if (h != sees.heads.end()) ++h->second;
+            else sees.heads.push_back({w, 1});
+        }
+    } catch (const std::bad_alloc&) {
+        return fail(HIKV_ERR_OUT_OF_MEMORY, "attend_window: host memory");
+    }
+    sees.kind = hides ? WindowMask::kind : CausalMask::kind;
+    return attend_call(c, layer, nq, total, q, out, sees, stream, "attend_window");
+}
+
+hikv_status hikv_attend_tree(hikv_cache* c, int32_t layer, const int32_t* nq, const uint32_t* mask, int32_t words,
+                             const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream) {
+    set_last_error("");
+    NvtxRange nvtx("hikv_attend_tree");
+    for (int b = 0; c && nq && b < c->B; ++b)
+        if (nq[b] > 32 * (int64_t)words)
+            return fail(HIKV_ERR_INVALID_ARG, "attend_tree: %d words a row for the %d nodes of batch row %d", words, nq[b], b);
+    int64_t total;
+    const hikv_status st = attend_check(c, layer, nq, q, out, &total, "attend_tree");
+    if (st != HIKV_OK || total == 0) return st;
+    if (!mask || ((uintptr_t)mask & 3)) return fail(HIKV_ERR_INVALID_ARG, "attend_tree: null or misaligned mask");
+    Sees sees;
+    sees.kind = TreeMask::kind;
+    sees.tree = {mask, words};
+    return attend_call(c, layer, nq, total, q, out, sees, stream, "attend_tree");
 }
 
 hikv_status hikv_drop(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* ndrop, hikv_stream_t stream) {

@@ -75,6 +75,26 @@ __device__ inline void reserve_unit(const View& v, int32_t u, int32_t ntok, int3
     v.next_pos[u] += ntok;
 }
 
+// Leave unit u its first `left` tokens, the next one to be at next_pos; with a
+// shared pool the whole pages past them go back.  One thread a unit; nothing may
+// take pages in the same launch.
+__device__ inline void shorten_unit(const View& v, int32_t u, int32_t left, int32_t next_pos) {
+    v.len[u] = left;
+    v.next_pos[u] = next_pos;
+    v.victim[u] = -1;
+    const int32_t keep = ceil_div(left, v.page_tokens), m = v.mapped[u];
+    if (v.home_pages || m <= keep) return;
+    const int32_t cnt = m - keep;
+    const int32_t old = atomicAdd(v.free_top, cnt);
+    if (old + cnt > v.pool_pages) atomicOr(v.err, DEVERR_POOL);
+    for (int32_t i = 0; i < cnt; ++i) {
+        const int64_t e = (int64_t)u * v.max_pages + keep + i;
+        if (old + i < v.pool_pages) v.free_stack[old + i] = v.page_table[e];
+        v.page_table[e] = -1;
+    }
+    v.mapped[u] = keep;
+}
+
 // 3-D tiled TMA load of box {x, y, z} of `tmap` into shared memory.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tmap, int32_t x, int32_t y, int32_t z,
                                             uint64_t* bar) {
@@ -141,6 +161,7 @@ struct PackedAppendArgs {
     int32_t pos0[kSeqMax];  // position of each sequence's first token
     int32_t base[kSeqMax];  // its slot, where the sequence's heads all hold as many tokens, else ...
     int32_t* reserved;      // ... scratch [units]: reserve slots and pages in a launch of their own (null: base)
+    const int32_t* depth;   // turn by the first token's position + depth[row], not by the token's own (null)
 };
 cudaError_t launch_append_packed(PackedAppendArgs& a, int dtype, int sm_count, cudaStream_t s);
 
@@ -187,13 +208,140 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
 __device__ __forceinline__ int32_t unit_len(const AttendArgs& a, int32_t i, int32_t u) {
     return a.len[i] >= 0 ? a.len[i] : a.v.len[u];
 }
+// What the queries of a call see (beside the slots up to the newest one).
+//
+// Causal: each query everything up to its own slot.
+struct CausalMask {
+    static constexpr int kind = 0;
+};
+// A window for every KV head: the newest window[g] slots up to the query's own,
+// and the first `sink`.  The keys of a work item are then numbered without the
+// slots between: number s is slot s below `gap` and slot s + shift from there
+// on, where gap is `sink` and gap + shift the first row's window start, both
+// rounded away from each other to multiples of `align` (the rows of a TMA box, 1
+// where rows are loaded one by one).  In these numbers a row's window is as
+// long as in slots, and no row sees a number from `sink` up to `gap`.
+constexpr int kAttHeads = 128;
+struct WindowMask {
+    static constexpr int kind = 1;
+    int32_t sink, align;
+    int32_t window[kAttHeads];   // all slots: kAllSlots
+};
+constexpr int32_t kAllSlots = 0x3FFFFFFF;
+// Trees: all slots in front of the sequence's new ones, and the new ones whose
+// bits are set in the row's words (bit j of word j / 32: new slot j).
+struct TreeMask {
+    static constexpr int kind = 2;
+    const uint32_t* bits;        // [packed rows][words]
+    int32_t words;
+};
+// the numbering of keys for rows from one that sees slots up to lim on
+template <class M>
+__device__ __forceinline__ void key_gap(const M& m, int32_t g, int32_t lim, int32_t& gap, int32_t& shift) {
+    gap = shift = 0;
+    if constexpr (M::kind == 1) {
+        const int32_t start = max(lim - m.window[g] + 1, 0) & -m.align;
+        gap = (m.sink + m.align - 1) & -m.align;
+        shift = max(start - gap, 0);
+    }
+}
+template <class M>
+__device__ __forceinline__ int32_t key_slot(int32_t s, int32_t gap, int32_t shift) {
+    return M::kind != 1 || s < gap ? s : s + shift;
+}
+// bits j < n of a word
+__device__ __forceinline__ uint32_t bits_below(int32_t n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+// What one row sees: word k of its visible keys from key number s0 on.
+template <class M>
+struct RowSight;
+template <>
+struct RowSight<CausalMask> {   // (the kernels compare with the row's last slot instead)
+    __device__ __forceinline__ RowSight(const CausalMask&, int32_t, int32_t, int32_t, int32_t, int32_t) {}
+};
+template <>
+struct RowSight<WindowMask> {
+    int32_t lim, from, sink;   // keys [from, lim], and below sink
+    __device__ __forceinline__ RowSight(const WindowMask& m, int32_t g, int32_t, int32_t, int32_t, int32_t row_lim)
+        : lim(row_lim), from(row_lim - m.window[g] + 1), sink(m.sink) {}
+    __device__ __forceinline__ uint32_t word(int32_t s0) const {
+        return bits_below(lim + 1 - s0) & (~bits_below(from - s0) | bits_below(sink - s0));
+    }
+};
+template <>
+struct RowSight<TreeMask> {
+    const uint32_t* bits;
+    int32_t seen0, nq;
+    __device__ __forceinline__ RowSight(const TreeMask& m, int32_t, int32_t packed_row, int32_t before, int32_t n, int32_t)
+        : bits(m.bits + (int64_t)packed_row * m.words), seen0(before), nq(n) {}
+    // word i of the row, with ones before the tree's first slot and zeros past its last
+    __device__ __forceinline__ uint32_t at(int32_t i) const {
+        if (i < 0) return 0xFFFFFFFFu;
+        return 32 * i < nq ? bits[i] & bits_below(nq - 32 * i) : 0u;
+    }
+    __device__ __forceinline__ uint32_t word(int32_t s0) const {
+        const int32_t b = s0 - seen0, i = b >> 5;   // (rounds down)
+        const uint32_t lo = at(i);
+        return b & 31 ? __funnelshift_r(lo, at(i + 1), b & 31) : lo;
+    }
+};
+
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
                              cudaStream_t s);
+cudaError_t launch_attend_tc_window(const AttendArgs& a, const WindowMask& m, const CUtensorMap& qmap,
+                                    const CUtensorMap& kvmap, int d, cudaStream_t s);
+cudaError_t launch_attend_tc_tree(const AttendArgs& a, const TreeMask& m, const CUtensorMap& qmap,
+                                  const CUtensorMap& kvmap, int d, cudaStream_t s);
 constexpr int kTcRows = 256, kTcKeys = 128;    // query rows of a work item of the bf16 kernel, keys per tile
 cudaError_t launch_attend_f32(const AttendArgs& a, int d, cudaStream_t s);
+cudaError_t launch_attend_f32_window(const AttendArgs& a, const WindowMask& m, int d, cudaStream_t s);
+cudaError_t launch_attend_f32_tree(const AttendArgs& a, const TreeMask& m, int d, cudaStream_t s);
 constexpr int kF32Rows = 128, kF32Keys = 64;   // of the fp32 kernel
 cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s);
+cudaError_t launch_attend_join_window(const AttendArgs& a, const WindowMask& m, int dtype, int d, cudaStream_t s);
+cudaError_t launch_attend_join_tree(const AttendArgs& a, const TreeMask& m, int dtype, int d, cudaStream_t s);
 cudaError_t launch_selftest_attend(const View& v, uint64_t limit_ns, cudaStream_t s);
+
+// Trees of drafted tokens (hikv_tree_masks): parents to ancestors' bits and depths.
+struct TreeArgs {
+    PackedSeqs seqs;
+    const int32_t* parent;
+    uint32_t* mask;
+    int32_t* depth;
+    int32_t words;
+    uint32_t* err;
+};
+cudaError_t launch_tree_masks(const TreeArgs& a, cudaStream_t s);
+
+// hikv_accept: parts of the batch rows' lists of kept tokens, at most one part of a row in a launch
+constexpr int kAcceptRows = 256, kAcceptIndex = 2048;
+struct AcceptArgs {
+    View v;
+    int32_t layer0, nlayers, n;
+    int32_t brow[kAcceptRows];
+    int32_t tree[kAcceptRows];           // newest tokens that the row's list is of
+    int32_t rank[kAcceptRows];           // place of this part's first token in the list
+    int32_t last[kAcceptRows];           // tokens the row keeps in all where this is its last part, else -1
+    int32_t start[kAcceptRows + 1];      // the part in index
+    int32_t index[kAcceptIndex];
+};
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
+
+// hikv_fork: copies of batch rows, grouped by the row they are of
+constexpr int kForkRows = 512, kForkSlots = 64;   // copies of a launch, slots of a CTA
+struct ForkArgs {
+    View v;
+    int32_t layer0, nlayers;
+    int32_t groups, copies;
+    int32_t chunks;                      // parts of kForkSlots slots of the longest source
+    int32_t src[kForkRows];              // [groups]
+    int32_t first[kForkRows + 1];        // [groups + 1] its copies
+    int32_t dst[kForkRows], same[kForkRows];
+};
+cudaError_t launch_fork_release(const ForkArgs& a, cudaStream_t s);   // shared pools, debug mode
+cudaError_t launch_fork_reserve(const ForkArgs& a, cudaStream_t s);   // shared pools
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s);
 
 constexpr int kDropMax = 512;
 struct DropArgs {

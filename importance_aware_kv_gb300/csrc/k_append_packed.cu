@@ -105,9 +105,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_append_packed(const __grid_c
     // (so far all of it was launch parameters)
     griddep_wait();   // the rows' producer, and whoever still reads the pages
     if (t >= a.seqs.start[a.seqs.n]) return;
+    int32_t at = p;   // the position to turn by
+    if (a.depth) {
+        const int32_t x = a.depth[t];
+        at = a.pos0[b] + min(max(x, 0), ntok - 1);   // (the host has checked that the tables reach ntok)
+        if (at != a.pos0[b] + x && lane == 0) atomicOr(v.err, DEVERR_STATE);
+    }
     if (rotates) {
-        const float* cp = a.cos + (int64_t)p * (a.rot / 2) + VE * pair;
-        const float* sp = a.sin + (int64_t)p * (a.rot / 2) + VE * pair;
+        const float* cp = a.cos + (int64_t)at * (a.rot / 2) + VE * pair;
+        const float* sp = a.sin + (int64_t)at * (a.rot / 2) + VE * pair;
 #pragma unroll
         for (int e = 0; e < VE; e += 4) {
             *reinterpret_cast<float4*>(c + e) = __ldg(reinterpret_cast<const float4*>(cp + e));
@@ -185,21 +191,7 @@ __global__ void __launch_bounds__(128) k_drop(const __grid_constant__ DropArgs a
         __syncwarp();
     }
     if (lane != 0) return;
-    v.len[u] = left;
-    v.next_pos[u] = c < 0 ? 0 : v.next_pos[u] - c;
-    v.victim[u] = -1;
-    const int32_t keep = ceil_div(left, v.page_tokens), m = v.mapped[u];
-    if (!v.home_pages && m > keep) {
-        const int32_t cnt = m - keep;
-        const int32_t old = atomicAdd(v.free_top, cnt);
-        if (old + cnt > v.pool_pages) atomicOr(v.err, DEVERR_POOL);
-        for (int32_t i = 0; i < cnt; ++i) {
-            const int64_t e = (int64_t)u * v.max_pages + keep + i;
-            if (old + i < v.pool_pages) v.free_stack[old + i] = v.page_table[e];
-            v.page_table[e] = -1;
-        }
-        v.mapped[u] = keep;
-    }
+    shorten_unit(v, u, left, c < 0 ? 0 : v.next_pos[u] - c);
 }
 
 }  // namespace

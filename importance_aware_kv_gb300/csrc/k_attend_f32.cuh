@@ -30,6 +30,11 @@
 // Non-finite V elements do not go through the products (0 x inf): they are
 // noted with their slots and added to the rows that see them.  A non-finite
 // element of k (or q) makes the logits of its key (or row) NaN.
+//
+// The same kernel serves sliding windows with visible first tokens and trees of
+// drafted tokens, as the bf16 kernel does (k_attend_tc.cuh).
+#pragma once
+
 #include "hikv_tcgen05.cuh"
 
 namespace hikv {
@@ -57,6 +62,7 @@ struct F3 {
     static constexpr int OFF_BAR = 4 * TILE;
     static constexpr int OFF_MISC = OFF_BAR + 14 * 8;     // tensor memory address, non-finite values noted
     static constexpr int OFF_WHERE = OFF_MISC + 8;        // where a wait gave up
+    static constexpr int OFF_EDGE = OFF_MISC + 12;        // non-finite values that not every row sees
     static constexpr int OFF_OVER = OFF_MISC + 16;        // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -104,8 +110,9 @@ __device__ __forceinline__ void mark_nan(float* x) {
         if (non_finite(x[i])) x[i] = __int_as_float(0x7FC00000);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constant__ AttendArgs a) {
+template <int D, class M>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attend_f32(const __grid_constant__ AttendArgs a, const __grid_constant__ M mask) {
     using C = F3<D>;
     extern __shared__ __align__(128) uint8_t raw[];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -121,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     uint64_t* drained = o_full + 1;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MISC);
     volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_WHERE);
+    volatile uint32_t* edge_bad = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_EDGE);
     int32_t* over = reinterpret_cast<int32_t*>(sm + C::OFF_OVER);
     const View& v = a.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
         mbar_init(o_full, 1);
         mbar_init(drained, 1);
         misc[1] = 0;
+        *edge_bad = 0;
         *where = 0;
         fence_mbar_init();
     }
@@ -159,8 +168,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * kRows;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i] * v.hkv + g;
     const int32_t n = unit_len(a, i, u);
-    const int32_t seen0 = n - nq;   // slots before the first query's own
-    const int32_t last_lim = seen0 + ((min(r0 + kRows, rows) - 1) >> a.gshift);   // what the last row sees
+    int32_t gap, shift;             // slot of key number s: s < gap ? s : s + shift (below, "slot" means number)
+    key_gap(mask, g, n - nq + (r0 >> a.gshift), gap, shift);
+    const int32_t seen0 = n - nq - shift;   // slots before the first query's own
+    const int32_t last_row = seen0 + ((min(r0 + kRows, rows) - 1) >> a.gshift);
+    const int32_t last_lim = M::kind == 2 ? n - 1 : last_row;   // what the last row sees
+    // whether every row sees all of slots [s, s + n) (masks other than the causal one)
+    auto all_see = [&](int32_t s, int32_t n) {
+        if constexpr (M::kind == 1)
+            return s + n - 1 <= seen0 + (r0 >> a.gshift) && (s > last_row - mask.window[g] || s + n - 1 < mask.sink);
+        return s + n <= seen0;
+    };
     const int32_t lo = splits > 1 ? split * a.chunk : 0;
     const int32_t end = splits > 1 ? min(last_lim + 1, lo + a.chunk) : last_lim + 1;
     const bool sane = n >= nq && n <= v.cap;
@@ -251,10 +269,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(s_read);   // the next tile's S may form
             const int32_t s0 = lo + t * kKeys;
-            if (s0 + kKeys - 1 > lim_w || s0 + kKeys > end) {
-                const int32_t left = min(lim, end - 1) - s0;   // columns [0, left] are seen
+            if constexpr (M::kind == 0) {
+                if (s0 + kKeys - 1 > lim_w || s0 + kKeys > end) {
+                    const int32_t left = min(lim, end - 1) - s0;   // columns [0, left] are seen
 #pragma unroll
-                for (int j = 0; j < 64; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
+                    for (int j = 0; j < 64; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
+                }
+            } else if (!all_see(s0, kKeys) || s0 + kKeys > end) {
+                const RowSight<M> sight(mask, g, first + (min(row, rows - 1) >> a.gshift), seen0, nq, lim);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t sees = sight.word(s0 + 32 * k) & bits_below(end - s0 - 32 * k);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[32 * k + j] = (sees >> j) & 1 ? s[32 * k + j] : 0xFF800000u;
+                }
             }
             float mx[4] = {m, m, m, m};
 #pragma unroll
@@ -319,8 +347,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                     if (over[2 * D + j] <= lim) x = __int_as_float(0x7FC00000);
                 }
             }
+            if constexpr (M::kind != 0) {
+                if (*edge_bad) {
+                    // (rare) the same for slots that not every row sees, one after the other
+                    const RowSight<M> sight(mask, g, first + (min(row, rows - 1) >> a.gshift), seen0, nq, lim);
+                    for (int32_t s = lo; s < end; ++s) {
+                        if (all_see(s, 1)) continue;
+                        const float* p = reinterpret_cast<const float*>(slot_row(v, u, key_slot<M>(s, gap, shift), true));
+                        if (!p || !(sight.word(s) & 1)) continue;
+#pragma unroll
+                        for (int j = 0; j < D / 2; ++j) {
+                            const float2 x = reinterpret_cast<const float2*>(p)[j];
+                            if (non_finite(x.x)) acc[j].x += x.x;
+                            if (non_finite(x.y)) acc[j].y += x.y;
+                        }
+                    }
+                }
+            }
             const bool wide = splits > 1 || (((uintptr_t)a.out.p | a.out.ts | a.out.hs) & 31) == 0;
-            const float inv = splits > 1 ? 1.f : 1.0f / l;
+            float inv = splits > 1 ? 1.f : 1.0f / l;
+            if (M::kind == 2 && splits == 1 && l == 0.f) inv = 0.f;   // a row that sees nothing
             const int32_t row4 = row & ~3;
             uint8_t* dst[4];   // lane k of each four writes the k-th 32 bytes of four rows' 128
 #pragma unroll
@@ -376,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const int32_t s = s0 + row_t + j * STEP;
-                    const uint8_t* p = s < end ? slot_row(v, u, s, is_v) : nullptr;
+                    const uint8_t* p = s < end ? slot_row(v, u, key_slot<M>(s, gap, shift), is_v) : nullptr;
                     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
                     *reinterpret_cast<float4*>(x[j]) = p ? reinterpret_cast<const float4*>(p)[2 * chunk] : z;
                     *reinterpret_cast<float4*>(x[j] + 4) = p ? reinterpret_cast<const float4*>(p)[2 * chunk + 1] : z;
@@ -398,8 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
                         for (int k = 0; k < 8; ++k) {
                             if (!non_finite(y[k])) continue;
                             const int kind = y[k] != y[k] ? 2 : (y[k] < 0.f ? 1 : 0);
-                            atomicMin(&over[kind * D + 8 * chunk + k], s0 + r);
                             y[k] = 0.f;
+                            if (M::kind != 0 && !all_see(s0 + r, 1)) {
+                                *edge_bad = 1;
+                                continue;
+                            }
+                            atomicMin(&over[kind * D + 8 * chunk + k], M::kind == 0 ? s0 + r : -1);
                             misc[1] = 1;
                         }
                         __threadfence_block();
@@ -469,17 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_f32(const __grid_constan
     }
 }
 
-template <int D>
-cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-    const cudaError_t e = func_smem_optin((const void*)k_attend_f32<D>, F3<D>::BYTES);
+template <int D, class M>
+cudaError_t launch_masked(const AttendArgs& a, const M& m, cudaStream_t s) {
+    const cudaError_t e = func_smem_optin((const void*)k_attend_f32<D, M>, F3<D>::BYTES);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(k_attend_f32<D>, a.items, kThreads, F3<D>::BYTES, s, a);
+    return launch_overlapped(k_attend_f32<D, M>, a.items, kThreads, F3<D>::BYTES, s, a, m);
 }
 
 }  // namespace
-
-cudaError_t launch_attend_f32(const AttendArgs& a, int d, cudaStream_t s) {
-    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
-}
-
 }  // namespace hikv

@@ -9,8 +9,8 @@ namespace {
 // split first: with m_s the parts' references, m the largest and f_s = 2^(m_s - m),
 //   o = sum_s f_s O_s / sum_s f_s l_s.
 // Bound by the latency of its three dependent reads (length, references, parts).
-template <typename T, int D>
-__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a) {
+template <typename T, int D, class M>
+__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs a, const __grid_constant__ M mask) {
     constexpr int E = D / 32;   // elements of a lane
     const View& v = a.v;
     const int32_t x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -22,8 +22,16 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     const int32_t i = prefix_find(a.comb0, a.nseq, tok);
     const int32_t j = tok - a.comb0[i];
     const int32_t n = unit_len(a, i, a.u0 + a.brow[i] * v.hkv + (h >> a.gshift));
-    const int32_t lim = n - a.nq[i] + j;   // the row sees slots [0, lim]
+    int32_t lim = n - a.nq[i] + j;   // the row sees no slot past lim
     if (lim < 0 || n > v.cap) return;
+    if constexpr (M::kind == 1) {    // in the key numbers of its work item
+        constexpr int rows = sizeof(T) == 2 ? kTcRows : kF32Rows;
+        const int32_t row = (j << a.gshift) + (h & ((1 << a.gshift) - 1)), r0 = row / rows * rows;
+        int32_t gap, shift;
+        key_gap(mask, h >> a.gshift, n - a.nq[i] + (r0 >> a.gshift), gap, shift);
+        lim -= shift;
+    }
+    if (M::kind == 2) lim = n - 1;
     const int32_t ns = min(lim / a.chunk + 1, a.splits);
     const int64_t row = (int64_t)(a.start[i] + j) * v.hq + h;
     float m = -INFINITY;
@@ -51,14 +59,18 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     if (gave_up) return;
     T* dst = reinterpret_cast<T*>(a.out.row(a.start[i] + j, h)) + lane * E;
 #pragma unroll
-    for (int k = 0; k < E; ++k) dst[k] = Elem<T>::from_f(o[k] / l);
+    for (int k = 0; k < E; ++k) dst[k] = Elem<T>::from_f(M::kind == 2 && l == 0.f ? 0.f : o[k] / l);
 }
 
-template <typename T>
-cudaError_t launch(const AttendArgs& a, int d, cudaStream_t s) {
+template <class M>
+cudaError_t launch(const AttendArgs& a, const M& m, int dtype, int d, cudaStream_t s) {
     const int32_t grid = (int32_t)(((int64_t)a.comb0[a.nseq] * a.v.hq + 3) / 4);
-    return d == 128 ? launch_overlapped(k_attend_join<T, 128>, grid, 128, 0, s, a)
-                    : launch_overlapped(k_attend_join<T, 64>, grid, 128, 0, s, a);
+    using B = __nv_bfloat16;
+    if (dtype == HIKV_BF16)
+        return d == 128 ? launch_overlapped(k_attend_join<B, 128, M>, grid, 128, 0, s, a, m)
+                        : launch_overlapped(k_attend_join<B, 64, M>, grid, 128, 0, s, a, m);
+    return d == 128 ? launch_overlapped(k_attend_join<float, 128, M>, grid, 128, 0, s, a, m)
+                    : launch_overlapped(k_attend_join<float, 64, M>, grid, 128, 0, s, a, m);
 }
 
 // one CTA whose wait on a barrier that nothing arrives on gives up after limit_ns
@@ -82,7 +94,13 @@ cudaError_t launch_selftest_attend(const View& v, uint64_t limit_ns, cudaStream_
 }
 
 cudaError_t launch_attend_join(const AttendArgs& a, int dtype, int d, cudaStream_t s) {
-    return dtype == HIKV_BF16 ? launch<__nv_bfloat16>(a, d, s) : launch<float>(a, d, s);
+    return launch(a, CausalMask{}, dtype, d, s);
+}
+cudaError_t launch_attend_join_window(const AttendArgs& a, const WindowMask& m, int dtype, int d, cudaStream_t s) {
+    return launch(a, m, dtype, d, s);
+}
+cudaError_t launch_attend_join_tree(const AttendArgs& a, const TreeMask& m, int dtype, int d, cudaStream_t s) {
+    return launch(a, m, dtype, d, s);
 }
 
 }  // namespace hikv

@@ -50,6 +50,15 @@
 // tiles need 2,048, and the chip runs at its power limit.  256 rows an item
 // because each key tile is then read from L2 once for two row tiles (64 KB a
 // step and SM; one row tile would double that to more than L2 delivers).
+//
+// The same kernel serves a sliding window a head with visible first tokens, and
+// trees of drafted tokens (CausalMask, WindowMask, TreeMask in hikv_packed.cuh).
+// A tile that not every row of the item sees whole, and only such a tile, is
+// masked by a word of bits for each 32 keys of a row, worked out by the row's
+// own thread; the keys between the first tokens and an item's window are left
+// out of its key numbers, so that they cost neither a load nor a product.
+#pragma once
+
 #include "hikv_tcgen05.cuh"
 
 namespace hikv {
@@ -104,11 +113,14 @@ struct __align__(16) Item {
     int32_t lo, end;         // keys [lo, end) of this split that any row sees
     int32_t nt0, nt1, ntiles;   // key tiles of each row tile, and of the item
     int32_t split;           // of the keys, -1: not split
-    int32_t u, pad[2];
+    int32_t u;
+    int32_t gap, shift;      // slot of key number s: s < gap ? s : s + shift
 };
 static_assert(sizeof(Item) == 64, "two items in OFF_ITEM");
-// item number `it` of the grid; false if it has nothing to do
-__device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item& w) {
+// item number `it` of the grid; false if it has nothing to do.  (Key numbers are
+// slots where no keys are left out; "slots" below means numbers.)
+template <class M>
+__device__ __forceinline__ bool load_item(const AttendArgs& a, const M& m, int32_t it, Item& w) {
     const View& v = a.v;
     const int32_t i = prefix_find(a.item0, a.nseq, it);
     const int32_t nq = a.nq[i];
@@ -129,11 +141,13 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item&
         return false;
     }
     w.seen0 = n - nq;
-    w.lim0 = w.seen0 + (w.r0 >> a.gshift);
+    key_gap(m, w.g, w.seen0 + (w.r0 >> a.gshift), w.gap, w.shift);
+    w.seen0 -= w.shift;
+    w.lim0 = M::kind == 2 ? w.seen0 - 1 : w.seen0 + (w.r0 >> a.gshift);
     w.lo = splits > 1 ? w.split * a.chunk : 0;
     auto keys_end = [&](int32_t a0) {   // one past the last key that the row tile from row a0 on sees
         if (a0 >= w.rows) return 0;
-        const int32_t hi = w.seen0 + ((min(a0 + 128, w.rows) - 1) >> a.gshift) + 1;
+        const int32_t hi = M::kind == 2 ? n : w.seen0 + ((min(a0 + 128, w.rows) - 1) >> a.gshift) + 1;
         return splits > 1 ? min(hi, w.lo + a.chunk) : hi;
     };
     const int32_t e0 = keys_end(w.r0), e1 = keys_end(w.r0 + 128);
@@ -143,8 +157,17 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, int32_t it, Item&
     w.ntiles = max(w.nt0, w.nt1);
     return w.ntiles > 0;
 }
-// tile t holds slots that the item's first row does not see, or that do not exist
-__device__ __forceinline__ bool edge_tile(const Item& w, int32_t t) { return w.lo + t * kKeys + kKeys - 1 > w.lim0; }
+// tile t holds slots that the item's first row (a row of it) does not see, or that do not exist
+template <class M>
+__device__ __forceinline__ bool edge_tile(const AttendArgs& a, const M& m, const Item& w, int32_t t) {
+    const int32_t s0 = w.lo + t * kKeys;
+    bool edge = s0 + kKeys - 1 > w.lim0;
+    if constexpr (M::kind == 1) {   // its last row's window starts last
+        const int32_t last = w.seen0 + ((min(w.r0 + kRows, w.rows) - 1) >> a.gshift);
+        edge |= s0 < last - m.window[w.g] + 1 && s0 + kKeys - 1 >= m.sink;
+    }
+    return edge;
+}
 
 // The work items of a CTA.  The grid has a CTA per item; a CTA that has
 // started takes the numbers of CTAs that have not, so the items go out one by
@@ -202,10 +225,41 @@ __device__ __forceinline__ int32_t read_next(uint32_t answer) {
     return ok ? (int32_t)x : -1;
 }
 
-template <int D>
+// (rare) Non-finite values of the edge tiles, for the rows that see them: warp 10
+// took them out of the products.  A whole warp, rows in its lanes; every lane
+// reads the same V element, so all take the same way.
+template <int D, class M>
+__device__ __noinline__ void add_non_finite(const AttendArgs& a, const M& m, const Item& w, int32_t nt,
+                                            const RowSight<M>& sight, uint32_t to) {
+    for (int32_t t = 0; t < nt; ++t) {
+        if (!edge_tile(a, m, w, t)) continue;
+        for (int32_t k = 0; k < kKeys; k += 32) {
+            const int32_t s0 = w.lo + t * kKeys + k;
+            const uint32_t sees = sight.word(s0);
+            for (int32_t j = 0; j < 32 && s0 + j < w.end; ++j) {
+                const int32_t s = s0 + j;
+                const uint8_t* p = slot_row(a.v, w.u, key_slot<M>(s, w.gap, w.shift), true);
+                if (!p) continue;
+#pragma unroll 1
+                for (int32_t i = 0; i < D; ++i) {
+                    const uint32_t x = reinterpret_cast<const uint16_t*>(p)[i];
+                    if ((x & 0x7F80u) != 0x7F80u) continue;
+                    __syncwarp();
+                    uint32_t o;
+                    tmem_ld1(o, to + i);
+                    const float y = __uint_as_float(o) + __uint_as_float(x << 16);
+                    tmem_st1(to + i, (sees >> j) & 1 ? __float_as_uint(y) : o);
+                    tmem_wait_st();
+                }
+            }
+        }
+    }
+}
+
+template <int D, class M>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
-                const __grid_constant__ CUtensorMap kvmap) {
+    k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ M mask,
+                const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap) {
     using C = Tc<D>;
     extern __shared__ __align__(128) uint8_t raw[];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -263,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();   // what the kernel before writes is there: lengths, pages, q
     Item w0;
     if (warp == 8) {
-        if (!load_item(a, blockIdx.x, w0)) w0.ntiles = 0;
+        if (!load_item(a, mask, blockIdx.x, w0)) w0.ntiles = 0;
         w0.some = !gave_up;
     }
     tc_fence_before();
@@ -289,6 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t lim = w.seen0 + (rc >> a.gshift);   // this row sees slots [0, lim]
             const int32_t lim_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3), w.rows - 1) >> a.gshift);
             const int32_t nt = tile ? w.nt1 : w.nt0;
+            auto sight = [&] {
+                return RowSight<M>(mask, w.g, w.first + (rc >> a.gshift), w.seen0, w.rows >> a.gshift, lim);
+            };
             float m = -INFINITY, l = 0.f;   // m: the maximum at the reference's last move
             float top = -INFINITY;          // the largest logit since
             auto reference = [&] { return m == -INFINITY ? 0.f : fmaf(m, c, kAhead); };
@@ -307,10 +364,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) held(s + 32 * j);
                 const int32_t s0 = w.lo + t * kKeys;
-                if (s0 + kKeys - 1 > lim_w) {
-                    const int32_t left = lim - s0;   // columns [0, left] are seen
+                if constexpr (M::kind == 0) {
+                    if (s0 + kKeys - 1 > lim_w) {
+                        const int32_t left = lim - s0;   // columns [0, left] are seen
 #pragma unroll
-                    for (int j = 0; j < 128; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
+                        for (int j = 0; j < 128; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
+                    }
+                } else if (edge_tile(a, mask, w, t)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t sees = sight().word(s0 + 32 * k);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[32 * k + j] = (sees >> j) & 1 ? s[32 * k + j] : 0xFF800000u;
+                    }
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
@@ -371,6 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ophase ^= 1;
                 tc_fence_after();
                 if (misc[2] == items.n) {
+                    if constexpr (M::kind != 0) {
+                        add_non_finite<D>(a, mask, w, nt, sight(), to);
+                    } else
                     // (rare) non-finite values of the edge tiles, for the rows that see them
 #pragma unroll 1
                     for (int j = 0; j < D; ++j) {
@@ -384,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                 }
-                const float inv = w.split < 0 ? 1.0f / l : 1.f;
+                float inv = w.split < 0 ? 1.0f / l : 1.f;
+                if (M::kind == 2 && w.split < 0 && l == 0.f) inv = 0.f;   // a row that sees nothing
                 // lane i of each four ends up with the i-th 32 bytes of four rows' 128
                 const int32_t row4 = row & ~3;
                 uint8_t* dst[4];
@@ -468,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++read;
                 const int32_t it = read_next(ans);
                 __syncwarp();
-                if (it < 0 || load_item(a, it, x)) {
+                if (it < 0 || load_item(a, mask, it, x)) {
                     x.some = it >= 0;
                     return;
                 }
@@ -516,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t s = s0 + box * bx;
                 int32_t pg = -1;
                 if (box < nb && s < w.end) {
-                    pg = unit_page(v, w.u, s);
+                    pg = unit_page(v, w.u, key_slot<M>(s, w.gap, w.shift));
                     if (pg < 0 || pg >= v.pool_pages) {
                         atomicOr(v.err, DEVERR_PAGE);
                         pg = -1;
@@ -527,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (pg >= 0)
                     tma_load_2d(sm + C::OFF_KV + st * C::TILE + hf * C::BLOCK + box * bx * 128, &kvmap, 64 * hf,
-                                (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens + (s & (v.page_tokens - 1))),
+                                (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens +
+                                          (key_slot<M>(s, w.gap, w.shift) & (v.page_tokens - 1))),
                                 &kv_full[st]);
             }
             w = next;
@@ -594,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = t + 1 < w.ntiles;
                     const int sv = r.st;   // V(t)
                     wait(&kv_full[sv], r.ph, 0x505);
-                    if (edge_tile(w, t)) {
+                    if (edge_tile(a, mask, w, t)) {
                         wait(&v_ok[sv], (vuse >> sv) & 1, 0x502);
                         vuse ^= 1u << sv;
                     }
@@ -643,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = fill % C::STAGES;
                 ok = warp_wait(&kv_full[st], (fill / C::STAGES) & 1, where, 0x600);
                 if (!ok) break;
-                if ((x & 1) && edge_tile(w, x >> 1)) {
+                if ((x & 1) && edge_tile(a, mask, w, x >> 1)) {
                     const int32_t s0 = w.lo + (x >> 1) * kKeys;
                     const int32_t rv = min(kKeys, w.end - s0);   // rows that hold visible tokens
                     uint8_t* tile = sm + C::OFF_KV + st * C::TILE;
@@ -682,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if ((y & 0x7F80) != 0x7F80) continue;
                                 const int r = i >> 6, col = 64 * hf + ((((i >> 3) & 7) ^ (r & 7)) << 3) + (i & 7);
                                 const int kind = (y & 0x7F) ? 2 : (y >> 15);
-                                atomicMin(&over[kind * D + col], s0 + r);
+                                if constexpr (M::kind == 0) atomicMin(&over[kind * D + col], s0 + r);
                                 *e = 0;
                             }
                         __syncwarp();
@@ -709,19 +780,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, cudaStream_t s) {
-    const void* f = (const void*)k_attend_tc<D>;
+template <int D, class M>
+cudaError_t launch_masked(const AttendArgs& a, const M& m, const CUtensorMap& qmap, const CUtensorMap& kvmap,
+                          cudaStream_t s) {
+    const void* f = (const void*)k_attend_tc<D, M>;
     cudaError_t e = func_smem_optin(f, Tc<D>::BYTES);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(k_attend_tc<D>, a.items, kThreads, Tc<D>::BYTES, s, a, qmap, kvmap);
+    return launch_overlapped(k_attend_tc<D, M>, a.items, kThreads, Tc<D>::BYTES, s, a, m, qmap, kvmap);
 }
 
 }  // namespace
-
-cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,
-                             cudaStream_t s) {
-    return d == 128 ? launch<128>(a, qmap, kvmap, s) : launch<64>(a, qmap, kvmap, s);
-}
-
 }  // namespace hikv

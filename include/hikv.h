@@ -386,6 +386,86 @@ hikv_status hikv_append_packed(hikv_cache* cache, int32_t layer, const int32_t* 
 hikv_status hikv_attend_packed(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const hikv_rows* q,
                                const hikv_rows* out, hikv_stream_t stream);
 
+/* hikv_attend_packed with a sliding window for every KV head (HOST window_host
+ * [num_kv_heads]; 0: none) and the first `sink` positions always visible: the
+ * query at position p sees, of the positions up to p, those > p - window_host[g]
+ * and those < sink (window 1 without sinks: its own token alone).
+ * Streaming heads beside retrieval heads (KV cache compression blog, sec. 3
+ * "StreamingLLM", "DuoAttention") in one call; keys that no query of a tile sees
+ * are neither loaded nor multiplied.  The cache is not cut by it.
+ * A unit that was cut can take a window that lies in the tokens appended since
+ * (nq + window - 1 of them), with sink <= the cache's num_sink; with window 0
+ * it is as by hikv_attend_packed.  Everything else as by hikv_attend_packed.
+ * Errors: as hikv_attend_packed, INVALID_ARG (null window_host, a negative window
+ * or sink), STATE (a cut unit and a window outside its newest tokens),
+ * UNSUPPORTED (more than 128 KV heads). */
+hikv_status hikv_attend_window(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const int32_t* window_host,
+                               int32_t sink, const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream);
+
+/* Trees of drafted tokens: a sequence adds ntok_host[b] nodes (HOST, [batch]),
+ * parents before children, one sequence after the other.  parent (DEVICE
+ * [sum ntok]) holds each node's parent as its number in its own sequence, -1 for
+ * a child of the last token before the tree.  Writes depth (DEVICE [sum ntok]; 0
+ * for parent -1) and mask (DEVICE [sum ntok][words]): bit j % 32 of word j / 32
+ * is set where node j lies on the node's path, the node itself included.  For
+ * one call a step, whose results serve every layer.
+ * A parent that is not an earlier node is taken as -1 and reported as
+ * HIKV_ERR_STATE by hikv_device_status.  parent, mask and depth must not overlap.
+ * May be captured.
+ * Errors: INVALID_ARG (null or misaligned pointers, a count negative or above 32 words). */
+hikv_status hikv_tree_masks(hikv_cache* cache, const int32_t* ntok_host, const int32_t* parent, uint32_t* mask,
+                            int32_t words, int32_t* depth, hikv_stream_t stream);
+
+/* hikv_append_packed of tree nodes: k and q are rotated by the position of the
+ * sequence's first node plus depth[row] (DEVICE [sum ntok], 0 <= depth < the
+ * sequence's ntok; others are clamped and reported as HIKV_ERR_STATE by
+ * hikv_device_status).  The nodes take the unit's next slots and, as far as the
+ * other calls are concerned, its next positions, in the order given, until
+ * hikv_accept or hikv_drop.
+ * Errors: as hikv_append_packed, INVALID_ARG (null depth or rope). */
+hikv_status hikv_append_tree(hikv_cache* cache, int32_t layer, const int32_t* ntok_host, const int32_t* depth,
+                             const hikv_rows* k, const hikv_rows* v, const hikv_rows* q, const hikv_rows* q_out,
+                             const hikv_rope* rope, hikv_stream_t stream);
+
+/* Attention of the newest nq_host[b] tokens of sequence b over everything in
+ * front of them and, among themselves, what mask says: bit j % 32 of word j / 32
+ * of a token's words (DEVICE [sum nq][words]) is set where it sees the j-th of
+ * the sequence's nq.  For the nodes of hikv_append_tree with the masks of
+ * hikv_tree_masks, or masks of the caller's own, in any shape; bits from nq_host[b]
+ * on are ignored.  A token that sees nothing (no bit set, nothing in front) gets
+ * a row of zeros.  Everything else as by hikv_attend_packed.
+ * Errors: as hikv_attend_packed, INVALID_ARG (null or misaligned mask, nq above 32 words). */
+hikv_status hikv_attend_tree(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const uint32_t* mask,
+                             int32_t words, const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream);
+
+/* Keep naccept_host[b] of the newest ntree_host[b] tokens of every unit of batch
+ * row b in the layer range, drop the others.  index_host (HOST, the rows' lists one
+ * after the other) names them by their number among the ntree_host[b], ascending;
+ * they move to the slots from the first of those on and hold the positions from
+ * its on, with their scores: what hikv_append_packed would have left, where they
+ * are a path of a tree from depth 0 on.  ntree 0 leaves a row alone.  One call for
+ * all layers, once the verified path is known.  All lists are HOST arrays read
+ * before the call returns.  With a shared pool whole pages past the remaining
+ * tokens return to it.  May be captured as hikv_append_packed.
+ * Errors: INVALID_ARG (counts, a list not ascending in [0, ntree)), STATE (ntree
+ * more than the unit holds newest tokens in order). */
+hikv_status hikv_accept(hikv_cache* cache, int32_t layer0, int32_t nlayers, const int32_t* ntree_host,
+                        const int32_t* naccept_host, const int32_t* index_host, hikv_stream_t stream);
+
+/* Make batch rows copies of others: every unit of row b in the layer range becomes
+ * what the same unit of row src_host[b] is (HOST [batch]; b or -1: the row stays) --
+ * tokens, scores, positions -- and what it held is gone.  For several samples of one
+ * prompt and for beam search, whose surviving beams keep their rows while dead
+ * ones take the copies.  A row that is copied cannot itself be a copy in the
+ * same call.  same_host (HOST [batch], or NULL: 0) promises that the first same_host[b] slots
+ * of row b hold the K and V that row src_host[b]'s do already, as after an earlier fork
+ * with no cut since; only the rows past them are copied (scores and positions all).
+ * May be captured as hikv_append_packed.
+ * Errors: INVALID_ARG (a row out of range, a copy of a copy, same_host above what
+ * either unit holds), CAPACITY (the page pool), OUT_OF_MEMORY (host memory). */
+hikv_status hikv_fork(hikv_cache* cache, int32_t layer0, int32_t nlayers, const int32_t* src_host,
+                      const int32_t* same_host, hikv_stream_t stream);
+
 /* Drop the newest tokens: ndrop_host[b] of every unit of batch row b in the
  * layer range (HOST, [batch]; -1: all the unit holds; ndrop_host NULL: -1 for
  * every row).  The dropped positions are free again: the next appended token
