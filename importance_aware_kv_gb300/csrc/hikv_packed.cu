@@ -494,6 +494,15 @@ hikv_status hikv_attend_window(hikv_cache* c, int32_t layer, const int32_t* nq, 
         return fail(HIKV_ERR_OUT_OF_MEMORY, "attend_window: host memory");
     }
     sees.kind = hides ? WindowMask::kind : CausalMask::kind;
+    std::sort(sees.heads.begin(), sees.heads.end(), [](const auto& x, const auto& y) { return x.first > y.first; });
+    WindowMask& m = sees.window;
+    int at = 0;
+    for (const auto& h : sees.heads) {
+        m.first[m.classes++] = (uint8_t)at;
+        for (int g = 0; g < c->Hkv; ++g)
+            if (m.window[g] == h.first) m.order[at++] = (uint8_t)g;
+    }
+    m.first[m.classes] = (uint8_t)at;
     return attend_call(c, layer, nq, total, q, out, sees, stream, "attend_window");
 }
 

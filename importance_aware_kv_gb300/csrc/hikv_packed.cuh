@@ -226,6 +226,8 @@ struct WindowMask {
     static constexpr int kind = 1;
     int32_t sink, align;
     int32_t window[kAttHeads];   // all slots: kAllSlots
+    int32_t classes;             // heads of equal windows, the longest first: heads order[first[c]] .. of class c
+    uint8_t first[kAttHeads + 1], order[kAttHeads];
 };
 constexpr int32_t kAllSlots = 0x3FFFFFFF;
 // Trees: all slots in front of the sequence's new ones, and the new ones whose
@@ -235,6 +237,22 @@ struct TreeMask {
     const uint32_t* bits;        // [packed rows][words]
     int32_t words;
 };
+// The head and the place among a head's items (of which there are `per`) of a
+// sequence's work item: heads in turn, but for windows of several lengths those of
+// the longest first, so that the longest items do not start last.
+template <class M>
+__device__ __forceinline__ void item_head(const AttendArgs& a, const M& m, int32_t item, int32_t per, int32_t& g, int32_t& x) {
+    if constexpr (M::kind == 1) {
+        int32_t c = 0;
+        while (c + 1 < m.classes && m.first[c + 1] * per <= item) ++c;
+        const int32_t heads = m.first[c + 1] - m.first[c], r = item - m.first[c] * per;
+        x = r / heads;
+        g = m.order[m.first[c] + r - x * heads];
+    } else {
+        x = a.hkv_shift >= 0 ? item >> a.hkv_shift : item / a.v.hkv;
+        g = item - x * a.v.hkv;
+    }
+}
 // the numbering of keys for rows from one that sees slots up to lim on
 template <class M>
 __device__ __forceinline__ void key_gap(const M& m, int32_t g, int32_t lim, int32_t& gap, int32_t& shift) {

@@ -164,8 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t i = prefix_find(a.item0, a.nseq, blockIdx.x);
     const int32_t nq = a.nq[i], first = a.start[i], rows = nq << a.gshift, tiles = ceil_div(rows, kRows);
     const int32_t splits = a.parts[i];
-    const int32_t rem = blockIdx.x - a.item0[i], g = rem % v.hkv, split = rem / v.hkv % splits;
-    const int32_t r0 = (tiles - 1 - rem / v.hkv / splits) * kRows;   // the last rows, which see most, first
+    int32_t g, x;
+    item_head(a, mask, blockIdx.x - a.item0[i], tiles * splits, g, x);
+    const int32_t split = x % splits;
+    const int32_t r0 = (tiles - 1 - x / splits) * kRows;   // the last rows, which see most, first
     const int32_t u = a.u0 + a.brow[i] * v.hkv + g;
     const int32_t n = unit_len(a, i, u);
     int32_t gap, shift;             // slot of key number s: s < gap ? s : s + shift (below, "slot" means number)

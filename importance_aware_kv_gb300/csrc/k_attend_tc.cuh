@@ -127,11 +127,11 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, const M& m, int32
     w.some = 1;
     w.rows = nq << a.gshift;
     const int32_t tiles = (w.rows + kRows - 1) / kRows;
-    const int32_t rem = it - a.item0[i], x = a.hkv_shift >= 0 ? rem >> a.hkv_shift : rem / v.hkv;
-    w.g = rem - x * v.hkv;
+    const int32_t splits = a.parts[i];
+    int32_t x;
+    item_head(a, m, it - a.item0[i], tiles * splits, w.g, x);
     w.u = a.u0 + a.brow[i] * v.hkv + w.g;
     const int32_t n = unit_len(a, i, w.u);
-    const int32_t splits = a.parts[i];
     const int32_t tile = splits > 1 ? x / splits : x;
     w.split = splits > 1 ? x - tile * splits : -1;
     w.r0 = (tiles - 1 - tile) * kRows;
@@ -512,8 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         // ---------------- TMA ----------------
         const int bx = min(v.page_tokens, 128), nb = 128 / bx;   // rows of a box, boxes of a tile
+        // pages at home, a box a page: slot s of unit u is row 2 (u rows_u + s) of the pool, its V row a box on
+        const bool home = v.home_pages && v.page_tokens <= 128;
+        const int32_t rows_u = v.max_pages << v.page_shift;
+        const int lane_row = lane / C::HALVES * bx, lane_x = 64 * (lane % C::HALVES);
+        uint8_t* lane_dst = sm + C::OFF_KV + lane % C::HALVES * C::BLOCK + lane_row * 128;
         const uint32_t ans = smem_u32(sm + C::OFF_ANSWER);
         uint32_t fill = 0, n = 0, asked = 0, read = 0;   // n: items handed out
+        Ring<C::STAGES> ring;
         bool ok = true;
         auto hand_out = [&](const Item& x) {
             const uint32_t s = n & 1;
@@ -554,7 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) hand_out(w);
         while (ok && w.some) {
             Item next;
-            const int32_t fills = 2 * w.ntiles, when = min(4, fills);
+            // The next item is asked for late, so that a CTA with a long item does not hold
+            // another one meanwhile, and read and handed out before it is loaded.
+            const int32_t fills = 2 * w.ntiles, when = M::kind == 0 ? min(4, fills) : min(fills, max(4, fills - 10));
+            const int32_t ask_at = max(1, fills - 14);
             for (int32_t x = 0; ok && x <= fills; ++x) {
                 if (x == when) {
                     next_item(next);
@@ -573,33 +582,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(sm + C::OFF_Q + t * C::TILE + hf * C::BLOCK, &qmap, 64 * hf, w.g << a.gshift,
                                     w.first + ((w.r0 + 128 * t) >> a.gshift), q_full);
                     }
-                    if (asked == read) ask();
+                    if (M::kind == 0 && asked == read) ask();
                 }
-                const int st = fill % C::STAGES;
-                const uint32_t use = fill / C::STAGES;
-                if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, where, 0x400 + st)) { ok = false; break; }
-                ++fill;
-                const bool is_v = x & 1;
-                const int32_t s0 = w.lo + (x >> 1) * kKeys;
-                // lane -> (box, half); a box wholly past the last visible slot is not loaded
-                const int box = lane / C::HALVES, hf = lane % C::HALVES;
-                const int32_t s = s0 + box * bx;
-                int32_t pg = -1;
-                if (box < nb && s < w.end) {
-                    pg = unit_page(v, w.u, key_slot<M>(s, w.gap, w.shift));
-                    if (pg < 0 || pg >= v.pool_pages) {
-                        atomicOr(v.err, DEVERR_PAGE);
-                        pg = -1;
+                if (M::kind != 0 && x == ask_at && asked == read) ask();
+                if constexpr (M::kind == 0) {
+                    const int st = fill % C::STAGES;
+                    const uint32_t use = fill / C::STAGES;
+                    if (use > 0 && !warp_wait(&kv_empty[st], (use - 1) & 1, where, 0x400 + st)) { ok = false; break; }
+                    ++fill;
+                    const bool is_v = x & 1;
+                    const int32_t s0 = w.lo + (x >> 1) * kKeys;
+                    // lane -> (box, half); a box wholly past the last visible slot is not loaded
+                    const int box = lane / C::HALVES, hf = lane % C::HALVES;
+                    const int32_t s = s0 + box * bx;
+                    int32_t pg = -1;
+                    if (box < nb && s < w.end) {
+                        pg = unit_page(v, w.u, s);
+                        if (pg < 0 || pg >= v.pool_pages) {
+                            atomicOr(v.err, DEVERR_PAGE);
+                            pg = -1;
+                        }
                     }
+                    const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], cnt * bx * 128);
+                    __syncwarp();
+                    if (pg >= 0)
+                        tma_load_2d(sm + C::OFF_KV + st * C::TILE + hf * C::BLOCK + box * bx * 128, &kvmap, 64 * hf,
+                                    (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens + (s & (v.page_tokens - 1))),
+                                    &kv_full[st]);
+                    continue;
                 }
-                const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                const int st = ring.st;
+                if (fill >= C::STAGES && !warp_wait(&kv_empty[st], ring.ph ^ 1, where, 0x400 + st)) { ok = false; break; }
+                ring.step();
+                ++fill;
+                // lane -> (box, half); a box wholly past the last visible slot is not loaded
+                const int32_t s = w.lo + (x >> 1) * kKeys + lane_row;
+                bool there = lane_row < kKeys && s < w.end;
+                const int32_t slot = key_slot<M>(s, w.gap, w.shift);
+                int32_t y = 2 * (w.u * rows_u + slot) + (x & 1) * bx;
+                if (!home && there) {
+                    const int32_t pg = unit_page(v, w.u, slot);
+                    there = pg >= 0 && pg < v.pool_pages;
+                    if (!there) atomicOr(v.err, DEVERR_PAGE);
+                    y = (int32_t)((2 * (int64_t)pg + (x & 1)) * v.page_tokens + (slot & (v.page_tokens - 1)));
+                }
+                const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, there));
                 if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], cnt * bx * 128);
                 __syncwarp();
-                if (pg >= 0)
-                    tma_load_2d(sm + C::OFF_KV + st * C::TILE + hf * C::BLOCK + box * bx * 128, &kvmap, 64 * hf,
-                                (int32_t)((2 * (int64_t)pg + (is_v ? 1 : 0)) * v.page_tokens +
-                                          (key_slot<M>(s, w.gap, w.shift) & (v.page_tokens - 1))),
-                                &kv_full[st]);
+                // (lanes that differ in their copies: one lane issuing all of a tile's took 12 % longer in all)
+                if (there) tma_load_2d(lane_dst + st * C::TILE, &kvmap, lane_x, y, &kv_full[st]);
             }
             w = next;
         }
