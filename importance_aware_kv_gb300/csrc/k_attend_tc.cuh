@@ -343,6 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t lim = w.seen0 + (rc >> a.gshift);   // this row sees slots [0, lim]
             const int32_t lim_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3), w.rows - 1) >> a.gshift);
             const int32_t nt = tile ? w.nt1 : w.nt0;
+            int32_t from_w = 0, mask_sink = 0;   // where the window of the warp's last row starts
+            if constexpr (M::kind == 1) {
+                from_w = w.seen0 + (min(w.r0 + 128 * tile + 32 * (warp & 3) + 31, w.rows - 1) >> a.gshift) - mask.window[w.g] + 1;
+                mask_sink = mask.sink;
+            }
             auto sight = [&] {
                 return RowSight<M>(mask, w.g, w.first + (rc >> a.gshift), w.seen0, w.rows >> a.gshift, lim);
             };
@@ -370,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 128; ++j) s[j] = j <= left ? s[j] : 0xFF800000u;
                     }
-                } else if (edge_tile(a, mask, w, t)) {
+                } else if (M::kind == 2 ? s0 + kKeys - 1 > w.lim0
+                                        : s0 + kKeys - 1 > lim_w || (s0 < from_w && s0 + kKeys - 1 >= mask_sink)) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t sees = sight().word(s0 + 32 * k);
@@ -433,6 +439,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             settle();
             if (nt > 0) {
+                float inv = w.split < 0 ? 1.0f / l : 1.f;
+                if (M::kind == 2 && w.split < 0 && l == 0.f) inv = 0.f;   // a row that sees nothing
+                // lane i of each four ends up with the i-th 32 bytes of four rows' 128
+                const int32_t row4 = row & ~3;
+                uint8_t* dst[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t tok = w.first + ((row4 + j) >> a.gshift);
+                    const int32_t h = (w.g << a.gshift) + ((row4 + j) & ((1 << a.gshift) - 1));
+                    dst[j] = (w.split < 0 ? a.out.row(tok, h)
+                                          : reinterpret_cast<uint8_t*>(
+                                                a.part + ((int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h) * D)) +
+                             32 * (lane & 3);
+                }
                 if (!warp_wait(&o_full[tile], ophase, where, 0x200)) { ok = false; break; }
                 ophase ^= 1;
                 tc_fence_after();
@@ -452,20 +472,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st1(to + j, __float_as_uint(x));
                     }
                     tmem_wait_st();
-                }
-                float inv = w.split < 0 ? 1.0f / l : 1.f;
-                if (M::kind == 2 && w.split < 0 && l == 0.f) inv = 0.f;   // a row that sees nothing
-                // lane i of each four ends up with the i-th 32 bytes of four rows' 128
-                const int32_t row4 = row & ~3;
-                uint8_t* dst[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t tok = w.first + ((row4 + j) >> a.gshift);
-                    const int32_t h = (w.g << a.gshift) + ((row4 + j) & ((1 << a.gshift) - 1));
-                    dst[j] = (w.split < 0 ? a.out.row(tok, h)
-                                          : reinterpret_cast<uint8_t*>(
-                                                a.part + ((int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h) * D)) +
-                             32 * (lane & 3);
                 }
                 // (not unrolled: an item runs this once, from a cold instruction cache)
                 if (w.split < 0) {
