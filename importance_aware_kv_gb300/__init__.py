@@ -13,6 +13,7 @@ import array
 import ctypes
 import os
 from dataclasses import dataclass
+from itertools import chain
 from typing import Optional, Sequence
 
 import numpy as np
@@ -207,7 +208,7 @@ class Tree:
     Cache.append_tree: ntok[b] nodes of sequence b, mask [sum ntok][words] int32
     (bit j % 32 of word j / 32: the node sees node j of its sequence), depth
     [sum ntok] int32 (append_tree only).  Cache.tree makes one from parents; masks
-    of any shape can be given here.  Keeps the tensors alive."""
+    of any shape can be given here.  Keeps a copy of ntok, and the tensors alive."""
 
     def __init__(self, ntok, mask, depth=None):
         import torch
@@ -218,8 +219,16 @@ class Tree:
             _dev(depth, "depth", torch.int32, mask.shape[:1])
             if depth.device != mask.device:
                 raise ValueError("mask and depth are on different devices")
-        self.ntok, self.mask, self.depth = ntok, mask, depth
+        self.ntok, self.mask, self.depth = tuple(getattr(ntok, "tolist", lambda: ntok)()), mask, depth
         self.device_index = mask.device.index
+        self.counts = None   # ntok as the C ABI takes it, once a cache has checked it
+
+    @classmethod
+    def _made(cls, ntok, mask, depth, device_index, counts):
+        """One whose tensors and counts a cache has made itself."""
+        t = cls.__new__(cls)
+        t.ntok, t.mask, t.depth, t.device_index, t.counts = tuple(ntok), mask, depth, device_index, counts
+        return t
 
 
 class _DeviceArray:
@@ -375,6 +384,7 @@ class Cache:
         import torch
         self.device_index = torch.cuda.current_device()
         self._torch_dtype = self._dtype()
+        self._int32 = torch.int32
         self._row_args = [hikv_rows() for _ in range(4)]   # k, v, q, q_out / out of a packed call
         self._row_refs = [ctypes.byref(r) for r in self._row_args]
 
@@ -506,36 +516,43 @@ class Cache:
         """The masks and depths of a batch of drafted trees: parent [sum ntok]
         int32 on the cache's device, each node's parent in its own sequence (an
         earlier node), -1 for a child of the last token before the tree."""
-        import torch
-        n, total, keep = self._counts(ntok, "ntok")
-        _dev(parent, "parent", torch.int32, (total,))
+        counts = n, total, keep = self._counts(ntok, "ntok")
+        if not getattr(parent, "is_cuda", False) or parent.dtype is not self._int32 or parent.shape != (total,) \
+                or not parent.is_contiguous():
+            import torch
+            _dev(parent, "parent", torch.int32, (total,))
         if parent.get_device() != self.device_index:
             raise ValueError(f"parent is on {parent.device}, the cache on cuda:{self.device_index}")
         words = max(1, -(-int(max(keep)) // 32))
         s = self._stream_int(stream)
-        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device=parent.device)):
-            mask = torch.empty(total, words, dtype=torch.int32, device=parent.device)
-            depth = torch.empty(total, dtype=torch.int32, device=parent.device)
+        if stream is None:
+            mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
+        else:   # memory of that stream's, so that no other one's work is still on it
+            import torch
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=parent.device)):
+                mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
         _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
-        return Tree(ntok, mask, depth)
+        return Tree._made(keep, mask, depth, self.device_index, counts)
 
-    def _tree(self, tree, total, name):
-        """A Tree's tensors checked against the packed rows of a call."""
+    def _tree(self, tree, name):
+        """A Tree's counts and one of its tensors, checked against this cache."""
         if tree.device_index != self.device_index:
             raise ValueError(f"the tree is on {tree.mask.device}, the cache on cuda:{self.device_index}")
+        if tree.counts is None or len(tree.ntok) != self.cfg.batch:
+            tree.counts = self._counts(tree.ntok, "ntok")
+        n, total, _ = tree.counts
         t = getattr(tree, name)
         if t is None:
             raise ValueError(f"the tree has no {name}")
         if t.shape[0] != total:
             raise ValueError(f"{name} has {t.shape[0]} rows, the tree {total} nodes")
-        return t.data_ptr()
+        return n, total, t.data_ptr()
 
     def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):
         """append_packed of a Tree's nodes, k (and q) rotated by the position of
         the sequence's first node plus the node's depth."""
         c = self.cfg
-        n, total, _keep = self._counts(tree.ntok, "ntok")
-        depth = self._tree(tree, total, "depth")
+        n, total, depth = self._tree(tree, "depth")
         rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
@@ -551,8 +568,7 @@ class Cache:
         everything in front of them and, among themselves, what the tree's masks
         say: q, out [sum ntok][Hq][d] as for attend_packed."""
         c = self.cfg
-        n, total, _keep = self._counts(tree.ntok, "ntok")
-        mask = self._tree(tree, total, "mask")
+        n, total, mask = self._tree(tree, "mask")
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
         _check(_lib.hikv_attend_tree(self.h, layer, n, mask, tree.mask.shape[1], rq, ro, self._stream_int(stream)))
 
@@ -560,12 +576,14 @@ class Cache:
         """Keep, of the newest ntree[b] tokens of batch row b, those that the
         list accepted[b] names (0 .. ntree[b] - 1, ascending), drop the others.
         ntree: counts, or the Tree."""
-        n, _, _keep = self._counts(ntree.ntok if isinstance(ntree, Tree) else ntree, "ntree")
+        if isinstance(ntree, Tree):
+            n, _, _keep = self._tree(ntree, "mask")
+        else:
+            n, _, _keep = self._counts(ntree, "ntree")
         if len(accepted) != self.cfg.batch:
             raise ValueError(f"accepted has {len(accepted)} lists, expected {self.cfg.batch}")
-        lists = [x if type(x) is list else list(x) for x in accepted]
-        counts = self._ints([len(x) for x in lists], "accepted", self.cfg.batch)
-        flat = [i for x in lists for i in x]
+        counts = array.array("i", map(len, accepted))
+        flat = list(chain.from_iterable(accepted))
         index = self._ints(flat, "accepted", len(flat))
         nl = self.cfg.num_layers - layer0 if nlayers is None else nlayers
         _check(_lib.hikv_accept(self.h, layer0, nl, n, counts.buffer_info()[0], index.buffer_info()[0],

@@ -333,7 +333,7 @@ struct TreeArgs {
 cudaError_t launch_tree_masks(const TreeArgs& a, cudaStream_t s);
 
 // hikv_accept: parts of the batch rows' lists of kept tokens, at most one part of a row in a launch
-constexpr int kAcceptRows = 256, kAcceptIndex = 2048;
+constexpr int kAcceptRows = 256, kAcceptIndex = 1024;
 struct AcceptArgs {
     View v;
     int32_t layer0, nlayers, n;
@@ -347,12 +347,14 @@ struct AcceptArgs {
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 
 // hikv_fork: copies of batch rows, grouped by the row they are of
-constexpr int kForkRows = 512, kForkSlots = 64;   // copies of a launch, slots of a CTA
+constexpr int kForkRows = 512;                        // copies of a launch
+constexpr int kForkSlots = 32, kForkMeta = 1024;      // slots of a CTA: K and V, scores and positions
 struct ForkArgs {
     View v;
     int32_t layer0, nlayers;
     int32_t groups, copies;
-    int32_t chunks;                      // parts of kForkSlots slots of the longest source
+    int32_t meta, chunks;                // parts of the longest source, of kForkMeta and of kForkSlots slots ...
+    int32_t from[kForkRows];             // ... [groups] from the first slot that a copy lacks on (whole parts)
     int32_t src[kForkRows];              // [groups]
     int32_t first[kForkRows + 1];        // [groups + 1] its copies
     int32_t dst[kForkRows], same[kForkRows];

@@ -42,20 +42,28 @@ hikv_status fork_launch(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t
     auto part = [&](size_t i0) {   // copies [i0, i0 + kForkRows)
         a.copies = (int32_t)std::min<size_t>(kForkRows, rows.size() - i0);
         a.groups = 0;
-        int longest = 0;
+        int longest = 0, rest = 0;   // slots of a source, and those that not every copy shares
         for (int i = 0; i < a.copies; ++i) {
             const int b = rows[i0 + i], s = src[b];
             if (i == 0 || s != a.src[a.groups - 1]) {
                 a.src[a.groups] = s;
+                a.from[a.groups] = INT32_MAX;
                 a.first[a.groups++] = i;
-                for (int l = layer0; l < layer0 + nl; ++l)
-                    for (int g = 0; g < c->Hkv; ++g) longest = std::max(longest, c->len[(l * c->B + s) * c->Hkv + g]);
             }
             a.dst[i] = b;
             a.same[i] = same ? same[b] : 0;
+            a.from[a.groups - 1] = std::min(a.from[a.groups - 1], a.same[i] / kForkSlots * kForkSlots);
         }
         a.first[a.groups] = a.copies;
-        a.chunks = std::max(1, ceil_div(longest, kForkSlots));
+        for (int x = 0; x < a.groups; ++x)
+            for (int l = layer0; l < layer0 + nl; ++l)
+                for (int g = 0; g < c->Hkv; ++g) {
+                    const int n = c->len[(l * c->B + a.src[x]) * c->Hkv + g];
+                    longest = std::max(longest, n);
+                    rest = std::max(rest, n - a.from[x]);
+                }
+        a.meta = std::max(1, ceil_div(longest, kForkMeta));
+        a.chunks = ceil_div(std::max(0, rest), kForkSlots);
     };
     // every page that goes back does so before the first is taken
     for (size_t i0 = 0; i0 < rows.size() && (!c->v.home_pages || c->v.debug); i0 += kForkRows) {
@@ -172,7 +180,8 @@ hikv_status hikv_accept(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t
     DeviceGuard guard(c->device);
     if (guard.status != cudaSuccess) return cuda_fail(guard.status, "accept: device");
     pdl_forget(c);
-    AcceptArgs a{};
+    AcceptArgs a;   // (its lists are filled as far as they are used)
+    a.n = a.start[0] = 0;
     a.v = c->v;
     a.layer0 = layer0;
     a.nlayers = nl;

@@ -2,7 +2,7 @@
 // rows are.
 //
 // A copy, bound by bytes: a source's K and V rows are read once for all its
-// copies and written once to each.  A CTA takes 64 slots of one unit of a
+// copies and written once to each.  A CTA takes 32 slots of one unit of a
 // source, every lane 16 bytes of several rows at once, and skips what a copy
 // shares with its source already.
 #include <algorithm>
@@ -52,64 +52,74 @@ __global__ void k_fork_reserve(const __grid_constant__ ForkArgs a) {
     if (n > v.len[u]) reserve_unit(v, u, n - v.len[u], &first);
 }
 
+// CTA per (source, layer, KV head, part): first the parts of the scores and
+// positions, then those of K and V
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) k_fork(const __grid_constant__ ForkArgs a) {
-    constexpr int BATCH = 4;
+    constexpr int BATCH = kForkSlots * 2 * VEC / kThreads;   // 16-byte columns of a lane, all in flight at once
     const View& v = a.v;
-    const int32_t per = a.chunks * v.hkv * a.nlayers;
-    const int32_t grp = blockIdx.x / per, rem = blockIdx.x % per;
-    const int32_t chunk = rem % a.chunks, g = rem / a.chunks % v.hkv, layer = a.layer0 + rem / a.chunks / v.hkv;
+    const int32_t parts = a.meta + a.chunks;
+    const int32_t part = blockIdx.x % parts, x = blockIdx.x / parts;
+    const int32_t g = x % v.hkv, y = x / v.hkv, layer = a.layer0 + y % a.nlayers, grp = y / a.nlayers;
+    const int32_t us = unit_of(v, layer, a.src[grp], g), c0 = a.first[grp], c1 = a.first[grp + 1];
     griddep_launch_dependents();
     griddep_wait();
-    const int32_t us = unit_of(v, layer, a.src[grp], g), n = v.len[us], next_pos = v.next_pos[us];
-    const int32_t c0 = a.first[grp], c1 = a.first[grp + 1];
+    const int32_t n = v.len[us];
     if (n > v.cap) {
         if (threadIdx.x == 0) atomicOr(v.err, DEVERR_STATE);
         return;
     }
-    if (chunk == 0 && threadIdx.x == 0) {
-        for (int32_t c = c0; c < c1; ++c) {
-            const int32_t u = unit_of(v, layer, a.dst[c], g);
-            v.len[u] = n;
-            v.next_pos[u] = next_pos;
-            v.victim[u] = -1;
+    if (part < a.meta) {
+        if (part == 0 && threadIdx.x == 0) {
+            const int32_t next_pos = v.next_pos[us];
+            for (int32_t c = c0; c < c1; ++c) {
+                const int32_t u = unit_of(v, layer, a.dst[c], g);
+                v.len[u] = n;
+                v.next_pos[u] = next_pos;
+                v.victim[u] = -1;
+            }
         }
-    }
-    const int32_t s0 = chunk * kForkSlots, s1 = min(s0 + kForkSlots, n);
-    for (int32_t s = s0 + threadIdx.x; s < s1; s += kThreads) {
-        const float x = v.imp[(int64_t)us * v.cap + s];
-        const int32_t p = v.pos[(int64_t)us * v.cap + s];
-        for (int32_t c = c0; c < c1; ++c) {
-            const int64_t m = (int64_t)unit_of(v, layer, a.dst[c], g) * v.cap + s;
-            v.imp[m] = x;
-            v.pos[m] = p;
+        const int32_t s0 = part * kForkMeta + threadIdx.x;
+        float imp[kForkMeta / kThreads];
+        int32_t pos[kForkMeta / kThreads];
+#pragma unroll
+        for (int k = 0; k < kForkMeta / kThreads; ++k) {
+            const int32_t s = s0 + k * kThreads;
+            if (s < n) {
+                imp[k] = v.imp[(int64_t)us * v.cap + s];
+                pos[k] = v.pos[(int64_t)us * v.cap + s];
+            }
         }
+        for (int32_t c = c0; c < c1; ++c) {
+            const int64_t at = (int64_t)unit_of(v, layer, a.dst[c], g) * v.cap;
+#pragma unroll
+            for (int k = 0; k < kForkMeta / kThreads; ++k) {
+                const int32_t s = s0 + k * kThreads;
+                if (s < n) {
+                    v.imp[at + s] = imp[k];
+                    v.pos[at + s] = pos[k];
+                }
+            }
+        }
+        return;
     }
-    int32_t lo = n;
-    for (int32_t c = c0; c < c1; ++c) lo = min(lo, a.same[c]);
-    lo = max(lo, s0);
-    if (lo >= s1) return;
-    const int32_t vec = v.row_bytes / 16, vshift = __ffs(vec) - 1;   // 16-byte columns of a row (8, 16 or 32)
-    const int32_t total = (s1 - lo) * 2 * vec;   // K rows, then V rows
-    for (int32_t i0 = threadIdx.x; i0 < total; i0 += BATCH * kThreads) {
-        uint4 x[BATCH];
+    const int32_t s0 = a.from[grp] + (part - a.meta) * kForkSlots;
+    if (s0 >= n) return;
+    // columns of the K rows, then of the V rows
+    uint4 d[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+        const int32_t i = threadIdx.x + k * kThreads, s = s0 + i / VEC % kForkSlots;
+        const uint8_t* p = s < n ? slot_row(v, us, s, i >= kForkSlots * VEC) : nullptr;
+        if (p) d[k] = reinterpret_cast<const uint4*>(p)[i % VEC];
+    }
+    for (int32_t c = c0; c < c1; ++c) {
+        const int32_t u = unit_of(v, layer, a.dst[c], g), same = a.same[c];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int32_t i = i0 + k * kThreads;
-            const bool is_v = i >= total / 2;
-            const int32_t e = is_v ? i - total / 2 : i;
-            const uint8_t* p = i < total ? slot_row(v, us, lo + (e >> vshift), is_v) : nullptr;
-            if (p) x[k] = reinterpret_cast<const uint4*>(p)[e & (vec - 1)];
-        }
-        for (int32_t c = c0; c < c1; ++c) {
-            const int32_t u = unit_of(v, layer, a.dst[c], g), same = a.same[c];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int32_t i = i0 + k * kThreads;
-                const bool is_v = i >= total / 2;
-                const int32_t e = is_v ? i - total / 2 : i, s = lo + (e >> vshift);
-                uint8_t* p = i < total && s >= same ? slot_row(v, u, s, is_v) : nullptr;
-                if (p) reinterpret_cast<uint4*>(p)[e & (vec - 1)] = x[k];
-            }
+            const int32_t i = threadIdx.x + k * kThreads, s = s0 + i / VEC % kForkSlots;
+            uint8_t* p = s < n && s >= same ? slot_row(v, u, s, i >= kForkSlots * VEC) : nullptr;
+            if (p) reinterpret_cast<uint4*>(p)[i % VEC] = d[k];
         }
     }
 }
@@ -127,8 +137,12 @@ cudaError_t launch_fork_reserve(const ForkArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s) {
-    const int64_t grid = (int64_t)a.groups * a.nlayers * a.v.hkv * a.chunks;
-    return launch_overlapped(k_fork, (int32_t)grid, kThreads, 0, s, a);
+    const int32_t grid = (int32_t)((int64_t)a.groups * a.nlayers * a.v.hkv * (a.meta + a.chunks));
+    switch (a.v.row_bytes) {
+        case 128: return launch_overlapped(k_fork<8>, grid, kThreads, 0, s, a);
+        case 256: return launch_overlapped(k_fork<16>, grid, kThreads, 0, s, a);
+        default: return launch_overlapped(k_fork<32>, grid, kThreads, 0, s, a);
+    }
 }
 
 }  // namespace hikv

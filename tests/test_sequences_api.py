@@ -23,7 +23,7 @@ def test_null_cache_is_refused(hk):
 
 
 class NoTree:
-    ntok, device_index, mask, depth = [1, 2], 0, torch.zeros(3, 1, dtype=torch.int32), None
+    ntok, device_index, mask, depth, counts = [1, 2], 0, torch.zeros(3, 1, dtype=torch.int32), None, None
 
 
 def test_lists_are_whole_numbers(cache):
