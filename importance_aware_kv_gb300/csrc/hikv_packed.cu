@@ -230,6 +230,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const AttendSeq* sq = seqs.data() + s0;
         a.chunk = attend_chunk(c, shape, sees, sq, a.nseq, total);
+        a.once = std::all_of(sq, sq + a.nseq, [&](const AttendSeq& s) { return (int64_t)s.nq * c->G <= shape.rows; });
         int64_t items = 0, split_tokens = 0, splits_max = 0;
         for (int i = 0; i < a.nseq; ++i) {
             const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;

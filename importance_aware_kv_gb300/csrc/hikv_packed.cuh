@@ -105,6 +105,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tmap, 
         : "memory");
 }
 
+// tma_load_2d with a policy for the lines that it brings into L2
+__device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* tmap, int32_t x, int32_t y, uint64_t* bar,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+        "%3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // packed fp32 pair addition
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     float2 d;
@@ -185,6 +195,7 @@ struct AttendArgs {
     int64_t part_rows;      // rows (t, h) of the packed batch
     int32_t splits;         // the most parts a sequence's keys are split into
     int32_t hkv_shift;      // log2 of the KV heads, -1: no power of two
+    int32_t once;           // every key is read by one work item
     int32_t nseq, items;
     int32_t brow[kAttSeqs];        // batch row
     int32_t start[kAttSeqs];       // first packed row

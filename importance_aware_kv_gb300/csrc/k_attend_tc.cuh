@@ -524,6 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lane_row = lane / C::HALVES * bx, lane_x = 64 * (lane % C::HALVES);
         uint8_t* lane_dst = sm + C::OFF_KV + lane % C::HALVES * C::BLOCK + lane_row * 128;
         const uint32_t ans = smem_u32(sm + C::OFF_ANSWER);
+        // Keys that one work item alone reads leave L2 first (64 tree nodes over eight
+        // 8K-32K caches 145 -> 140 us); those that many read stay (evict_first for a 16K
+        // prompt in windows of 1024: 216 us instead of 203).
+        uint64_t policy = 0;
+        if constexpr (M::kind != 0) {
+            if (a.once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+            else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+        }
         uint32_t fill = 0, n = 0, asked = 0, read = 0;   // n: items handed out
         Ring<C::STAGES> ring;
         bool ok = true;
@@ -637,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], cnt * bx * 128);
                 __syncwarp();
                 // (lanes that differ in their copies: one lane issuing all of a tile's took 12 % longer in all)
-                if (there) tma_load_2d(lane_dst + st * C::TILE, &kvmap, lane_x, y, &kv_full[st]);
+                if (there) tma_load_2d_hint(lane_dst + st * C::TILE, &kvmap, lane_x, y, &kv_full[st], policy);
             }
             w = next;
         }
