@@ -509,8 +509,8 @@ class Cache:
             window = [window] * c.num_kv_heads
         w = self._ints(window, "window", c.num_kv_heads)
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
-        _check(_lib.hikv_attend_window(self.h, layer, n, w.buffer_info()[0], int(sink), rq, ro,
-                                       self._stream_int(stream)))
+        sink = min(max(int(sink), -1), 0x7FFFFFFF)
+        _check(_lib.hikv_attend_window(self.h, layer, n, w.buffer_info()[0], sink, rq, ro, self._stream_int(stream)))
 
     def tree(self, parent, ntok, stream=None):
         """The masks and depths of a batch of drafted trees: parent [sum ntok]

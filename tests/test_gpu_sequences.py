@@ -245,7 +245,7 @@ def bits_of(m, words):
 
 def tree_sees(masks, held):
     def sees(b, g, n, pos):
-        t = masks[b].shape[0]
+        t = masks[b].shape[0]   # (whatever the unit holds in front of them)
         return torch.cat([torch.ones(t, n - t, dtype=torch.bool, device=DEV), masks[b].to(DEV)], 1)
     return sees
 
@@ -633,6 +633,176 @@ def test_fork_of_more_rows_than_a_launch_takes(hk):
     for b in range(0, B, 7):
         for x, y in zip(slots(cache, b), rows[b // 100]):
             assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------------------
+# together, strided, far, in debug mode
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d,hq,hkv,off", [("bf16", 128, 8, 2, 8), ("bf16", 64, 4, 4, 8), ("f32", 64, 8, 1, 4)])
+def test_strided_rows_and_what_lies_around_them(hk, dtype, d, hq, hkv, off):
+    """q as slices of a projection's output, outputs at 16-byte offsets with
+    strides of their own: nothing beside the rows is written."""
+    new, held = [37, 0, 70, 1], [300, 20, 5, 64]
+    cache = make(hk, 4, hq, hkv, d, dtype, 384)
+    gen, cpu = gen_of(61), torch.Generator().manual_seed(13)
+    fill(cache, gen, (held, new))
+    total = sum(new)
+    q = rnd(gen, total, (hq + 2 * hkv) * d, dtype=dtype)[:, :hq * d].unflatten(1, (hq, d))
+    parents = [random_tree(cpu, n) for n in new]
+    tree = cache.tree(torch.tensor(sum(parents, []), dtype=torch.int32, device=DEV), new)
+    for call, sees in ((lambda o: cache.attend_window(q, o, new, 50, 3), window_sees(new, [50] * hkv, 3)),
+                       (lambda o: cache.attend_tree(q, o, tree), tree_sees([paths_of(p) for p in parents], held))):
+        room = torch.full((total + 2, hq * d + 3 * off), 7.0, device=DEV, dtype=DT[dtype])
+        out = room[1:-1, off:off + hq * d].unflatten(1, (hq, d))
+        call(out)
+        check(cache, q, out, new, sees)
+        out.fill_(7.0)
+        assert bool((room == 7.0).all())
+
+
+def test_tree_over_pages_of_any_size(hk):
+    for dtype, page, shared in (("bf16", 16, True), ("bf16", 32, False), ("bf16", 256, True), ("f32", 16, True)):
+        new, held = [70, 1, 33], [333, 800, 5]
+        kw = dict(pool_pages=3 * 2 * -(-832 // page) - 1) if shared else {}
+        cache = make(hk, 3, 8, 2, 128, dtype, 832, page_tokens=page, **kw)
+        gen, cpu = gen_of(62 + page), torch.Generator().manual_seed(14)
+        for n in ([100, 7, 0], [233, 793, 5], new):   # shared: the rows' pages interleave
+            fill(cache, gen, [n])
+        masks = [torch.rand(n, n, generator=cpu) < 0.5 for n in new]
+        tree = hk.Tree(new, torch.cat([bits_of(m, 3) for m in masks]).to(DEV))
+        q, out = queries(cache, gen, sum(new))
+        cache.attend_tree(q, out, tree)
+        check(cache, q, out, new, tree_sees(masks, held))
+        old = [slots(cache, u) for u in range(6)]
+        keep = [[0, 1, 5, 40, 69], [], [3, 32]]
+        cache.accept(tree, keep)
+        for u in range(6):
+            idx = list(range(held[u // 2])) + [held[u // 2] + i for i in keep[u // 2]]
+            k, v, p = slots(cache, u)
+            assert torch.equal(k, old[u][0][idx]) and torch.equal(v, old[u][1][idx]) and p.tolist() == list(range(len(idx)))
+        cache.device_status()
+
+
+def test_tree_over_a_cut_unit(hk):
+    gen, cpu = gen_of(63), torch.Generator().manual_seed(15)
+    cache = make(hk, 2, 8, 2, 64, "bf16", 512, budgets=[100, 60], num_sink=4, recent_window=16)
+    fill(cache, gen, [[300, 40]])
+    cache.evict()
+    fill(cache, gen, [[20, 9]])
+    masks = [torch.rand(n, n, generator=cpu) < 0.5 for n in (20, 9)]
+    tree = hk.Tree([20, 9], torch.cat([bits_of(m, 1) for m in masks]).to(DEV))
+    q, out = queries(cache, gen, 29)
+    cache.attend_tree(q, out, tree)
+    check(cache, q, out, [20, 9], tree_sees(masks, None))
+    cache.accept(tree, [[2, 3], [8]])
+    assert cache.lengths().tolist() == [102, 62, 41, 41]
+    with pytest.raises(hk.HikvError) as e:
+        cache.accept([3, 0], [[0], []])   # the cut has left two in order
+    assert e.value.status == hk.HIKV_ERR_STATE
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_fork_tree_and_steps_together(hk, dtype):
+    """A prompt read in windows, forked, drafted and verified by trees, decoded
+    on: copies that are given the same stay the same as their source, and as a
+    cache that was never forked."""
+    hq, hkv, d, n = 8, 2, 64, 150
+    a, b = make(hk, 3, hq, hkv, d, dtype, 256, page_tokens=16), make(hk, 3, hq, hkv, d, dtype, 256)
+    gen, cpu = gen_of(64), torch.Generator().manual_seed(16)
+    rope = hk.Rope(*tables(256, d))
+    qkv = rnd(gen, n, hq + 2 * hkv, d, dtype=dtype)
+    for c in (a, b):
+        rows = [n, 0, 0] if c is a else [n] * 3
+        x = qkv if c is a else qkv.repeat(3, 1, 1)
+        q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+        qo, out = torch.empty_like(x[:, :hq]), torch.empty_like(x[:, :hq])
+        c.append_packed(k, v, rows, q=q, q_out=qo, rope=rope)
+        c.attend_window(qo, out, rows, 40, 4)
+        check(c, qo, out, rows, window_sees(rows, [40] * hkv, 4))
+    a.fork([0, 0, 0])
+    for step in range(3):
+        m = (7, 33, 1)[step]
+        parent = random_tree(cpu, m)
+        path = [i for i in range(m) if paths_of(parent)[-1, i]]
+        flat = torch.tensor(parent * 3, dtype=torch.int32, device=DEV)
+        x = rnd(gen, m, hq + 2 * hkv, d, dtype=dtype).repeat(3, 1, 1)
+        q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+        outs = []
+        for c in (a, b):
+            qo, out = torch.empty_like(x[:, :hq]), torch.empty_like(x[:, :hq])
+            tree = c.tree(flat, [m] * 3)
+            c.append_tree(k, v, tree, rope, q=q, q_out=qo)
+            c.attend_tree(qo, out, tree)
+            c.accept(tree, [path] * 3)
+            outs.append(out)
+        assert torch.equal(*outs) and torch.equal(outs[0][:m], outs[0][m:2 * m]) and torch.equal(outs[0][:m], outs[0][2 * m:])
+    q1, kv = rnd(gen, 1, 1, hq, d, dtype=dtype).repeat(1, 3, 1, 1), rnd(gen, 1, 1, hkv, 1, d, dtype=dtype).repeat(1, 3, 1, 1, 1)
+    o1, o2 = torch.empty_like(q1), torch.empty_like(q1)
+    for _ in range(3):
+        a.step(kv, kv, q1, o1)
+        b.step(kv, kv, q1, o2)
+        assert torch.equal(o1, o2) and torch.equal(o1[0, 0], o1[0, 2])
+    for x, y in zip(a.gather(with_kv=True), b.gather(with_kv=True)):
+        assert torch.equal(x, y)
+    a.device_status()
+
+
+def test_calls_at_offsets_past_32_bits(hk):
+    """A pool of 5 GiB: the last row's pages lie past 2^32 bytes."""
+    B, n = 40, 30000
+    cache = make(hk, B, 32, 8, 128, "bf16", 32768)
+    assert cache.device_view()["pages"].numel() * 2 >= 5 << 30
+    gen, cpu = gen_of(65), torch.Generator().manual_seed(17)
+    zeros = [0] * (B - 1)
+    fill(cache, gen, [[n] + zeros])
+    cache.fork([-1] * (B - 1) + [0])
+    for g in range(8):
+        for x, y in zip(slots(cache, g), slots(cache, (B - 1) * 8 + g)):
+            assert torch.equal(x, y)
+    new = zeros + [20]
+    fill(cache, gen, [new])
+    parent = random_tree(cpu, 20)
+    tree = cache.tree(torch.tensor(parent, dtype=torch.int32, device=DEV), new)
+    q, out = queries(cache, gen, 20)
+    cache.attend_tree(q, out, tree)
+    check(cache, q, out, new, tree_sees([torch.zeros(0, 0)] * (B - 1) + [paths_of(parent)], None))
+    cache.attend_window(q, out, new, 5000, 4)
+    check(cache, q, out, new, window_sees(new, [5000] * 8, 4))
+    old = slots(cache, (B - 1) * 8 + 7)
+    cache.accept(tree, [[]] * (B - 1) + [[4, 19]])
+    k, v, _ = slots(cache, (B - 1) * 8 + 7)
+    idx = list(range(n)) + [n + 4, n + 19]
+    assert torch.equal(k, old[0][idx]) and torch.equal(v, old[1][idx])
+    cache.device_status()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_vacated_slots_in_debug_mode(hk, shared, monkeypatch):
+    """Slots that acceptance and forks give up read as NaN, and nothing that
+    is seen does."""
+    monkeypatch.setenv("HIKV_DEBUG", "1")
+    kw = dict(page_tokens=16, pool_pages=3 * 2 * 20 - 1) if shared else {}
+    cache = make(hk, 3, 4, 2, 64, "bf16", 320, **kw)
+    monkeypatch.delenv("HIKV_DEBUG")
+    gen = gen_of(66)
+    fill(cache, gen, [[100, 300, 20], [40, 0, 0]])
+    w = cache.device_view()
+    cache.accept([40, 0, 20], [[3, 9], [], []])
+    cache.fork([0, 0, 0])
+    assert cache.lengths().tolist() == [102] * 6
+    for b in range(3):
+        for g in (0, 1):
+            u = 2 * b + g
+            k, v, _ = slots(cache, u)
+            assert bool(torch.isfinite(k).all() and torch.isfinite(v).all())
+            if b != 2:                              # (row 2 was shorter before)
+                assert bool(torch.isnan(w["importance"][u, 102:140]).all()) and bool((w["positions"][u, 102:140] == -1).all())
+            if not shared and b != 2:
+                assert math.isnan(cache.read_slot(u, 102)[2])
+    q, out = queries(cache, gen, 6)
+    cache.attend_window(q, out, [2, 2, 2], 30, 4)
+    check(cache, q, out, [2, 2, 2], window_sees([2, 2, 2], [30, 30], 4))
+    cache.device_status()
 
 
 # ---------------------------------------------------------------------------
