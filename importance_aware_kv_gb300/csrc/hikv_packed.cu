@@ -100,15 +100,18 @@ int64_t item_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, con
     const int64_t start = std::max<int64_t>(s.n - s.nq + t * k.rows / c->G - window + 1, 0) / align * align;
     return seen - std::max<int64_t>(start - gap, 0);
 }
-// the most keys of a work item of a sequence
-int64_t most_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq& s) {
+// the most keys of a work item of a sequence, for heads of one window and for all
+int64_t most_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq& s, int32_t window) {
     if (sees.kind != WindowMask::kind) return s.n;
     const int64_t tiles = ((int64_t)s.nq * c->G + k.rows - 1) / k.rows;
-    int64_t most = 0;
-    for (const auto& h : sees.heads)   // the last tiles span most keys; the last but one may have more rows
-        for (int64_t t = std::max<int64_t>(0, tiles - 2); t < tiles; ++t)
-            most = std::max(most, item_keys(c, k, sees, s, t, h.first));
+    int64_t most = 0;   // the last tiles span most keys; the last but one may have more rows
+    for (int64_t t = std::max<int64_t>(0, tiles - 2); t < tiles; ++t) most = std::max(most, item_keys(c, k, sees, s, t, window));
     return std::min<int64_t>(most + sees.window.align, s.n);   // (windows of inner tiles may start lower in a box)
+}
+int64_t most_keys(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq& s) {
+    int64_t most = 0;
+    for (const auto& h : sees.heads) most = std::max(most, most_keys(c, k, sees, s, h.first));
+    return most;
 }
 
 // Keys per split, a multiple of the keys of a step (INT32_MAX: no split).
@@ -159,6 +162,88 @@ int32_t attend_chunk(const hikv_cache* c, const ItemShape& k, const Sees& sees, 
         }
     }
     return best_chunk;
+}
+
+// When the last of the items given out one by one, longest first, is done: `items`
+// of (steps, count) in descending order.
+double rounds(const std::vector<std::pair<double, int64_t>>& items, int64_t slots) {
+    std::vector<std::pair<double, int64_t>> busy{{0.0, slots}};   // until when, slots; ascending
+    for (auto [len, n] : items)
+        while (n > 0) {
+            auto [at, have] = busy.front();
+            const int64_t m = std::min(n, have);
+            if (m == have) busy.erase(busy.begin());
+            else busy.front().second -= m;
+            const auto to = std::lower_bound(busy.begin(), busy.end(), at + len, [](const auto& x, double y) { return x.first < y; });
+            if (to != busy.end() && to->first == at + len) to->second += m;
+            else busy.insert(to, {at + len, m});
+            n -= m;
+        }
+    return busy.back().first;
+}
+
+// Windows and trees with a few more work items than SMs: the sequences that fill
+// whole rounds stay whole, the others' keys are split to fill the last one.  64
+// single tokens in windows of 2044 (512 items of 17 steps, 32/8 heads): 99.5 us, all
+// whole 104.  With 256 rows an item partial results cost what it gains (60 tree nodes of
+// twelve sequences, 192 items, 64/8 heads: 53 us whole, 60 split).
+// Returns how many of the first sequences stay whole, *chunk keys per split of
+// the others; all of them and INT32_MAX where that does not pay.
+int attend_tail(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq* sq, int nseq, int32_t* chunk) {
+    const int64_t slots = c->sm_count;
+    *chunk = INT32_MAX;
+    std::vector<std::pair<double, int64_t>> all;   // (steps, items) of every sequence and window
+    std::vector<int> of;                           // its sequence
+    int64_t items = 0, most = 0;
+    int whole = 0;
+    for (int i = 0; i < nseq; ++i) {
+        const int64_t tiles = ((int64_t)sq[i].nq * c->G + k.rows - 1) / k.rows;
+        items += tiles * c->Hkv;
+        for (const auto& h : sees.heads) {
+            const int64_t keys = most_keys(c, k, sees, sq[i], h.first);
+            all.push_back({(double)((keys + k.keys - 1) / k.keys), tiles * h.second});
+            of.push_back(i);
+            most = std::max(most, keys);
+        }
+    }
+    if (items <= slots || items >= 4 * slots) return nseq;
+    int64_t full = 0;
+    for (; whole < nseq; ++whole) {
+        const int64_t n = (((int64_t)sq[whole].nq * c->G + k.rows - 1) / k.rows) * c->Hkv;
+        if (full + n > items / slots * slots) break;
+        full += n;
+    }
+    const int64_t maxsteps = (most + k.keys - 1) / k.keys;
+    auto cost = [&](int first, int64_t ct) {   // sequences from `first` on split into parts of ct steps
+        std::vector<std::pair<double, int64_t>> parts;
+        for (size_t x = 0; x < all.size(); ++x) {
+            const auto [st, n] = all[x];
+            if (of[x] < first || st <= ct) parts.push_back({st + k.item_steps, n});
+            else {
+                const int64_t p = (int64_t)st / ct;
+                parts.push_back({ct + k.item_steps, p * n});
+                if (st - p * ct > 0) parts.push_back({st - p * ct + k.item_steps, n});
+            }
+        }
+        std::sort(parts.begin(), parts.end(), [](const auto& x, const auto& y) { return x.first > y.first; });
+        return rounds(parts, slots);
+    };
+    double best = cost(nseq, maxsteps);
+    int best_whole = nseq;
+    int64_t tokens = 0;
+    for (int i = whole; i < nseq; ++i) tokens += sq[i].nq;
+    for (const int parts : {2, 3, 4}) {
+        const int64_t ct = (maxsteps + parts - 1) / parts, splits = (maxsteps + ct - 1) / ct;
+        const int64_t partial = splits * tokens * c->Hq * (c->d + 2);
+        if (ct < 2 || partial > c->attend_room) break;
+        const double x = cost(whole, ct) + k.join_steps + 8.0 * partial / k.step_bytes;
+        if (x < best) {
+            best = x;
+            best_whole = whole;
+            *chunk = (int32_t)(ct * k.keys);
+        }
+    }
+    return best_whole;
 }
 
 cudaError_t launch_kernels(const hikv_cache* c, const Sees& sees, const AttendArgs& a, const CUtensorMap& qmap, cudaStream_t s) {
@@ -230,11 +315,14 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.nseq = (int32_t)std::min<size_t>(kAttSeqs, seqs.size() - s0);
         const AttendSeq* sq = seqs.data() + s0;
         a.chunk = attend_chunk(c, shape, sees, sq, a.nseq, total);
+        int whole = 0;   // of the first sequences, those that stay whole
+        if (sees.kind != CausalMask::kind && a.chunk == INT32_MAX)
+            whole = attend_tail(c, shape, sees, sq, a.nseq, &a.chunk);
         a.once = std::all_of(sq, sq + a.nseq, [&](const AttendSeq& s) { return (int64_t)s.nq * c->G <= shape.rows; });
         int64_t items = 0, split_tokens = 0, splits_max = 0;
         for (int i = 0; i < a.nseq; ++i) {
             const int64_t tiles = ((int64_t)sq[i].nq * c->G + shape.rows - 1) / shape.rows;
-            const int64_t splits = (most_keys(c, shape, sees, sq[i]) + a.chunk - 1) / a.chunk;
+            const int64_t splits = i < whole ? 1 : (most_keys(c, shape, sees, sq[i]) + a.chunk - 1) / a.chunk;
             a.brow[i] = sq[i].brow;
             a.start[i] = sq[i].start;
             a.nq[i] = sq[i].nq;
@@ -250,6 +338,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
         a.item0[a.nseq] = a.items = (int32_t)items;
         a.comb0[a.nseq] = (int32_t)split_tokens;
         a.splits = (int32_t)splits_max;
+        if (sees.kind != CausalMask::kind) a.part_rows = split_tokens * c->Hq;
         a.part = c->d_logits;
         a.part_ml = c->d_logits + splits_max * a.part_rows * c->d;
         cudaError_t e = launch_kernels(c, sees, a, qmap, (cudaStream_t)stream);

@@ -192,7 +192,7 @@ struct AttendArgs {
     int32_t chunk;          // keys per split (a multiple of the kernel's key tile)
     float* part;            // partial results of split items: [splits][part_rows][d] outputs, ...
     float* part_ml;         // ... [splits][part_rows][2] references and sums
-    int64_t part_rows;      // rows (t, h) of the packed batch
+    int64_t part_rows;      // rows (t, h) of the packed batch; windows and trees: of its split sequences
     int32_t splits;         // the most parts a sequence's keys are split into
     int32_t hkv_shift;      // log2 of the KV heads, -1: no power of two
     int32_t once;           // every key is read by one work item
@@ -215,6 +215,8 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* first, int32_t n, 
     }
     return lo;
 }
+// windows and trees: from a packed row of sequence i to its place among the split sequences' tokens
+__device__ __forceinline__ int32_t part_token(const AttendArgs& a, int32_t i) { return a.comb0[i] - a.start[i]; }
 // tokens of unit u, of sequence i of the call
 __device__ __forceinline__ int32_t unit_len(const AttendArgs& a, int32_t i, int32_t u) {
     return a.len[i] >= 0 ? a.len[i] : a.v.len[u];

@@ -370,13 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             float inv = splits > 1 ? 1.f : 1.0f / l;
             if (M::kind == 2 && splits == 1 && l == 0.f) inv = 0.f;   // a row that sees nothing
             const int32_t row4 = row & ~3;
+            const int32_t pt = M::kind != 0 ? part_token(a, i) : 0;   // of a token in the partial results, from its packed row
             uint8_t* dst[4];   // lane k of each four writes the k-th 32 bytes of four rows' 128
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int32_t tok = first + ((row4 + j) >> a.gshift);
                 const int32_t h = (g << a.gshift) + ((row4 + j) & ((1 << a.gshift) - 1));
                 dst[j] = (splits > 1 ? reinterpret_cast<uint8_t*>(
-                                           a.part + ((int64_t)split * a.part_rows + (int64_t)tok * v.hq + h) * D)
+                                           a.part + ((int64_t)split * a.part_rows + (int64_t)(tok + pt) * v.hq + h) * D)
                                      : a.out.row(tok, h)) +
                          32 * (lane & 3);
             }
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (splits > 1 && row < rows) {
                 const int32_t tok = first + (row >> a.gshift), h = (g << a.gshift) + (row & ((1 << a.gshift) - 1));
-                const int64_t pr = (int64_t)split * a.part_rows + (int64_t)tok * v.hq + h;
+                const int64_t pr = (int64_t)split * a.part_rows + (int64_t)(tok + pt) * v.hq + h;
                 *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m * c, l);
             }
         }

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
     }
     if (M::kind == 2) lim = n - 1;
     const int32_t ns = min(lim / a.chunk + 1, a.splits);
-    const int64_t row = (int64_t)(a.start[i] + j) * v.hq + h;
+    const int64_t row = (int64_t)(M::kind == 0 ? a.start[i] + j : tok) * v.hq + h;
     float m = -INFINITY;
     for (int32_t s = lane; s < ns; s += 32) m = fmaxf(m, a.part_ml[(s * a.part_rows + row) * 2]);
 #pragma unroll

@@ -107,7 +107,7 @@ struct Ring {
 
 // A work item, the same in every warp
 struct __align__(16) Item {
-    int32_t some;            // 0: there is none left
+    int32_t some;            // 0: there is none left; else the sequence, from 1 on
     int32_t g, first, rows;  // KV head, first packed row, query rows of the sequence
     int32_t r0, seen0, lim0; // first row; slots before the first query's own; last slot the first row sees
     int32_t lo, end;         // keys [lo, end) of this split that any row sees
@@ -124,7 +124,7 @@ __device__ __forceinline__ bool load_item(const AttendArgs& a, const M& m, int32
     const View& v = a.v;
     const int32_t i = prefix_find(a.item0, a.nseq, it);
     const int32_t nq = a.nq[i];
-    w.some = 1;
+    w.some = M::kind == 0 ? 1 : i + 1;
     w.rows = nq << a.gshift;
     const int32_t tiles = (w.rows + kRows - 1) / kRows;
     const int32_t splits = a.parts[i];
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item w0;
     if (warp == 8) {
         if (!load_item(a, mask, blockIdx.x, w0)) w0.ntiles = 0;
-        w0.some = !gave_up;
+        if (gave_up) w0.some = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -443,6 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (M::kind == 2 && w.split < 0 && l == 0.f) inv = 0.f;   // a row that sees nothing
                 // lane i of each four ends up with the i-th 32 bytes of four rows' 128
                 const int32_t row4 = row & ~3;
+                int32_t pt = 0;   // of a token in the partial results, from its packed row
+                if (M::kind != 0 && w.split >= 0) pt = part_token(a, w.some - 1);
                 uint8_t* dst[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t h = (w.g << a.gshift) + ((row4 + j) & ((1 << a.gshift) - 1));
                     dst[j] = (w.split < 0 ? a.out.row(tok, h)
                                           : reinterpret_cast<uint8_t*>(
-                                                a.part + ((int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h) * D)) +
+                                                a.part + ((int64_t)w.split * a.part_rows + (int64_t)(tok + pt) * v.hq + h) * D)) +
                              32 * (lane & 3);
                 }
                 if (!warp_wait(&o_full[tile], ophase, where, 0x200)) { ok = false; break; }
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (w.split >= 0 && row < w.rows) {
                     const int32_t tok = w.first + (row >> a.gshift), h = (w.g << a.gshift) + (row & ((1 << a.gshift) - 1));
-                    const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)tok * v.hq + h;
+                    const int64_t pr = (int64_t)w.split * a.part_rows + (int64_t)(tok + pt) * v.hq + h;
                     *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m == -INFINITY ? m : reference(), l);
                 }
             }
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t it = read_next(ans);
                 __syncwarp();
                 if (it < 0 || load_item(a, mask, it, x)) {
-                    x.some = it >= 0;
+                    if (it < 0) x.some = 0;
                     return;
                 }
                 ask();

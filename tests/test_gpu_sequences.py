@@ -510,6 +510,30 @@ def test_step_in_a_graph(hk):
                 assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("kind", ["window", "tree"])
+def test_last_sequences_split_when_rounds_do_not_fill(hk, kind):
+    """A few more work items than whole rounds of them: the shortest sequences'
+    keys are split, the others' not, each into its own rows."""
+    B, hq, hkv = 40, 16, 8
+    held = [1700 + 11 * ((17 * b) % B) for b in range(B)]
+    new = [0 if b == 5 else 1 + b % 2 for b in range(B)]
+    cache = make(hk, B, hq, hkv, 64, "bf16", 2176)
+    gen, cpu = gen_of(38), torch.Generator().manual_seed(18)
+    fill(cache, gen, (held, new))
+    q, out = queries(cache, gen, sum(new))
+    before = cache.kernel_launches()
+    if kind == "window":
+        cache.attend_window(q, out, new, 1500, 4)
+        sees = window_sees(new, [1500] * hkv, 4)
+    else:
+        masks = [torch.rand(n, n, generator=cpu) < 0.6 for n in new]
+        cache.attend_tree(q, out, hk.Tree(new, torch.cat([bits_of(m, 1) for m in masks]).to(DEV)))
+        sees = tree_sees(masks, held)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert cache.kernel_launches() - before == 2   # 312 items on 152 SMs
+    check(cache, q, out, new, sees)
+
+
 # ---------------------------------------------------------------------------
 # copies
 # ---------------------------------------------------------------------------
