@@ -13,7 +13,8 @@
 // moves to base + j.  The list ascends, so index[j] >= j and a destination is
 // never a later entry's source: a warp a unit, whose lanes each own 16-byte
 // columns of the K and V rows, can load several entries ahead of their stores
-// without a barrier.
+// without a barrier.  Bound by latency as well: four of 32 nodes in 512 units take
+// 5 to 6 us, the masks of those 2,048 nodes 3.4.
 #include "hikv_packed.cuh"
 
 namespace hikv {
