@@ -226,6 +226,11 @@ int attend_tail(const hikv_cache* c, const ItemShape& k, const Sees& sees, const
             }
         }
         std::sort(parts.begin(), parts.end(), [](const auto& x, const auto& y) { return x.first > y.first; });
+        size_t n = 0;   // those of a length as one
+        for (const auto& p : parts)
+            if (n > 0 && parts[n - 1].first == p.first) parts[n - 1].second += p.second;
+            else parts[n++] = p;
+        parts.resize(n);
         return rounds(parts, slots);
     };
     double best = cost(nseq, maxsteps);

@@ -247,6 +247,15 @@ __device__ __noinline__ void add_non_finite(const AttendArgs& a, const M& m, con
                 if (!p) continue;
 #pragma unroll 1
                 for (int32_t i = 0; i < D; ++i) {
+                    if ((i & 7) == 0) {   // eight finite ones at once
+                        const uint4 y = *reinterpret_cast<const uint4*>(p + 2 * i);
+                        const uint32_t top = __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                                      __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+                        if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) {
+                            i += 7;
+                            continue;
+                        }
+                    }
                     const uint32_t x = reinterpret_cast<const uint16_t*>(p)[i];
                     if ((x & 0x7F80u) != 0x7F80u) continue;
                     __syncwarp();

@@ -432,8 +432,8 @@ hikv_status hikv_append_tree(hikv_cache* cache, int32_t layer, const int32_t* nt
  * of a token's words (DEVICE [sum nq][words]) is set where it sees the j-th of
  * the sequence's nq.  For the nodes of hikv_append_tree with the masks of
  * hikv_tree_masks, or masks of the caller's own, in any shape; bits from nq_host[b]
- * on are ignored.  A token that sees nothing (no bit set, nothing in front) gets
- * a row of zeros.  Everything else as by hikv_attend_packed.
+ * on are ignored; mask must not overlap out.  A token that sees nothing (no bit set,
+ * nothing in front) gets a row of zeros.  Everything else as by hikv_attend_packed.
  * Errors: as hikv_attend_packed, INVALID_ARG (null or misaligned mask, nq above 32 words). */
 hikv_status hikv_attend_tree(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const uint32_t* mask,
                              int32_t words, const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream);
