@@ -227,7 +227,7 @@ class Tree:
     def _made(cls, ntok, mask, depth, device_index, counts):
         """One whose tensors and counts a cache has made itself."""
         t = cls.__new__(cls)
-        t.ntok, t.mask, t.depth, t.device_index, t.counts = tuple(ntok), mask, depth, device_index, counts
+        t.ntok, t.mask, t.depth, t.device_index, t.counts = ntok, mask, depth, device_index, counts
         return t
 
 
@@ -523,7 +523,7 @@ class Cache:
             _dev(parent, "parent", torch.int32, (total,))
         if parent.get_device() != self.device_index:
             raise ValueError(f"parent is on {parent.device}, the cache on cuda:{self.device_index}")
-        words = max(1, -(-int(max(keep)) // 32))
+        words = max(1, -(-int(max(ntok if type(ntok) is list else keep)) // 32))
         s = self._stream_int(stream)
         if stream is None:
             mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
