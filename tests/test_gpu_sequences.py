@@ -347,6 +347,20 @@ def test_tree_hides_what_is_not_finite(hk, dtype):
     check(cache, q, out, new, tree_sees([m], held))
 
 
+@pytest.mark.parametrize("dtype,d,hq,hkv", [("bf16", 128, 8, 2), ("f32", 64, 4, 2)])
+def test_long_masks(hk, dtype, d, hq, hkv):
+    """Masks of many words a row: most key tiles are the tree's own."""
+    new, held = [1500, 0, 333], [100, 7, 2000]
+    gen, cpu = gen_of(39), torch.Generator().manual_seed(19)
+    cache = make(hk, 3, hq, hkv, d, dtype, 2368)
+    fill(cache, gen, (held, new))
+    masks = [torch.rand(n, n, generator=cpu) < 0.2 for n in new]
+    tree = hk.Tree(new, torch.cat([bits_of(m, 48) for m in masks]).to(DEV))
+    q, out = queries(cache, gen, sum(new))
+    cache.attend_tree(q, out, tree)
+    check(cache, q, out, new, tree_sees(masks, held))
+
+
 def test_bad_parents_are_reported(hk):
     cache = make(hk, 2, 4, 2, 64, "bf16", 64)
     parent = torch.tensor([-1, 0, 2, 9, -2, 0, 0], dtype=torch.int32, device=DEV)   # nodes 2, 3 and 4 of the first
@@ -885,6 +899,23 @@ def test_refusals_leave_the_cache_as_it_was(hk):
     assert cache.kernel_launches() == before
     assert cache.lengths().tolist() == [45, 45, 5, 5]
     cache.device_status()
+
+
+def test_windows_of_many_heads(hk):
+    """128 KV heads in 16 windows; more are refused."""
+    cache = make(hk, 1, 128, 128, 64, "bf16", 96)
+    gen = gen_of(55)
+    fill(cache, gen, [[70], [20]])
+    windows = [(7 * g) % 16 * 5 for g in range(128)]
+    q, out = queries(cache, gen, 20)
+    cache.attend_window(q, out, [20], windows, 1)
+    check(cache, q, out, [20], window_sees([20], windows, 1))
+    cache = make(hk, 1, 129, 129, 64, "bf16", 16)
+    fill(cache, gen, [[2]])
+    q, out = queries(cache, gen, 1)
+    with pytest.raises(hk.HikvError) as e:
+        cache.attend_window(q, out, [1], 1)
+    assert e.value.status == hk.HIKV_ERR_UNSUPPORTED
 
 
 def test_depths_out_of_range_are_reported(hk):
