@@ -92,7 +92,7 @@ struct Tc {
     static constexpr int OFF_ANSWER = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // of the work distributor, 16 bytes
     static constexpr int OFF_ITEM = OFF_ANSWER + 16;      // two work items
     static constexpr int OFF_MISC = OFF_ITEM + 2 * 64;    // tensor memory address, epilogue count, overlay item, turn
-    static constexpr int OFF_WHERE = OFF_MISC + 16;       // where a wait gave up
+    static constexpr int OFF_WHERE = OFF_MISC + 16;       // where a wait gave up; epilogue count of row tile 1
     static constexpr int OFF_OVER = OFF_WHERE + 16;       // [3][D] first slots of +inf, -inf, NaN
     static constexpr int BYTES = OFF_OVER + 3 * D * 4 + 1024;
 };
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], kReaders);
         }
-        misc[1] = 0;                      // epilogues done, in warps
+        misc[1] = where[1] = 0;           // epilogues of row tile 0 and 1 done, in warps
         misc[3] = 0;                      // a row tile is issuing the products between two of its softmaxes
         *where = 0;
         misc[2] = 0;                      // the item that `over` belongs to, from 1 on
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) atomicAdd(const_cast<uint32_t*>(&misc[1]), 1u);
+            if (lane == 0) atomicAdd(const_cast<uint32_t*>(tile ? &where[1] : &misc[1]), 1u);
         }
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -794,9 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
                     if (__any_sync(0xffffffffu, bad)) {
                         if (misc[2] != items.n) {
-                            // `over` is free once every epilogue before this item has read it
+                            // `over` is free once every epilogue before this item has read it.  (Counted
+                            // by row tile: the warps of one without rows are ahead of the other's by items.)
                             const uint64_t t0 = global_ns();
-                            while (misc[1] < 8 * seen) {
+                            while (misc[1] < 4 * seen || where[1] < 4 * seen) {
                                 if (global_ns() - t0 > kWaitLimitNs) {
                                     *where = 0x601;
                                     ok = false;

@@ -548,6 +548,36 @@ def test_last_sequences_split_when_rounds_do_not_fill(hk, kind):
     check(cache, q, out, new, sees)
 
 
+@pytest.mark.parametrize("call", ["packed", "window", "tree"])
+def test_non_finite_values_of_every_item_arrive(hk, call):
+    """More short items of one row tile than SMs, each with a non-finite value
+    in its last tile: the rows get their own, whichever items a CTA takes in
+    turn."""
+    B, hkv, n = 60, 8, 90
+    cache = make(hk, B, 16, hkv, 64, "bf16", 128)
+    gen = gen_of(40)
+    fill(cache, gen, [[n] * B])
+    w = cache.device_view()
+    u = torch.arange(B * hkv, device=DEV)
+    slot, col = n - 1 - u % 30, u % 64
+    value = torch.tensor([math.inf, -math.inf, math.nan], device=DEV)[u % 3]
+    pt = w["pages"].shape[2]
+    w["pages"][w["page_table"][u, slot // pt].long(), 1, slot % pt, col] = value.bfloat16()
+    q, out = queries(cache, gen, B)
+    tree = hk.Tree([1] * B, torch.ones(B, 1, dtype=torch.int32, device=DEV))
+    run = {"packed": lambda: cache.attend_packed(q, out, [1] * B), "window": lambda: cache.attend_window(q, out, [1] * B, 60, 2),
+           "tree": lambda: cache.attend_tree(q, out, tree)}[call]
+    for _ in range(30):
+        out.fill_(7.0)
+        run()
+        got = out.view(B * hkv, 2, 64)
+        want = torch.zeros(B * hkv, 64, device=DEV)
+        want[u, col] = value
+        bad = ~torch.isfinite(want)[:, None].expand_as(got)
+        assert bool(torch.isfinite(got[~bad]).all())
+        assert torch.equal(got[bad].float().nan_to_num(9.0), want[:, None].expand_as(got)[bad].nan_to_num(9.0))
+
+
 # ---------------------------------------------------------------------------
 # copies
 # ---------------------------------------------------------------------------
