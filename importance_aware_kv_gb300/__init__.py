@@ -534,7 +534,7 @@ class Cache:
         _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
         return Tree._made(keep, mask, depth, self.device_index, counts)
 
-    def _tree(self, tree, name):
+    def _tree(self, tree, name, stream=None):
         """A Tree's counts and one of its tensors, checked against this cache."""
         if tree.device_index != self.device_index:
             raise ValueError(f"the tree is on {tree.mask.device}, the cache on cuda:{self.device_index}")
@@ -546,13 +546,16 @@ class Cache:
             raise ValueError(f"the tree has no {name}")
         if t.shape[0] != total:
             raise ValueError(f"{name} has {t.shape[0]} rows, the tree {total} nodes")
+        if stream is not None:   # (the tensor's memory is another stream's, perhaps)
+            import torch
+            t.record_stream(torch.cuda.ExternalStream(self._stream_int(stream), device=t.device))
         return n, total, t.data_ptr()
 
     def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):
         """append_packed of a Tree's nodes, k (and q) rotated by the position of
         the sequence's first node plus the node's depth."""
         c = self.cfg
-        n, total, depth = self._tree(tree, "depth")
+        n, total, depth = self._tree(tree, "depth", stream)
         rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
@@ -568,7 +571,7 @@ class Cache:
         everything in front of them and, among themselves, what the tree's masks
         say: q, out [sum ntok][Hq][d] as for attend_packed."""
         c = self.cfg
-        n, total, mask = self._tree(tree, "mask")
+        n, total, mask = self._tree(tree, "mask", stream)
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
         _check(_lib.hikv_attend_tree(self.h, layer, n, mask, tree.mask.shape[1], rq, ro, self._stream_int(stream)))
 

@@ -233,7 +233,7 @@ hikv_status hikv_fork(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* 
     if (!range_ok(c, layer0, nl)) return fail(HIKV_ERR_INVALID_ARG, "fork: bad cache or layer range");
     if (!src) return fail(HIKV_ERR_INVALID_ARG, "fork: null src");
     bool any = false;
-    int64_t pages = 0;
+    int64_t pages = 0, longest = 0;
     for (int b = 0; b < c->B; ++b) {
         const int s = src[b];
         if (s < -1 || s >= c->B) return fail(HIKV_ERR_INVALID_ARG, "fork: batch row %d of row %d", b, s);
@@ -248,12 +248,15 @@ hikv_status hikv_fork(hikv_cache* c, int32_t layer0, int32_t nl, const int32_t* 
                     return fail(HIKV_ERR_INVALID_ARG, "fork: %d tokens of batch row %d are not to be copied, unit %d holds %d and unit %d %d",
                                 same[b], b, u, c->len[u], from, c->len[from]);
                 const int need = ceil_div(c->len[from], c->P);
+                longest = std::max<int64_t>(longest, c->len[from]);
                 if (c->v.home_pages) continue;
                 pages += c->len[u] > c->len[from] ? std::min(c->mapped[u], need) - c->mapped[u]
                                                   : std::max(c->mapped[u], need) - c->mapped[u];
             }
     }
     if (!any) return HIKV_OK;
+    if ((longest / kForkSlots + longest / kForkMeta + 2) * std::min(kForkRows, c->B) * nl * c->Hkv > INT32_MAX)
+        return fail(HIKV_ERR_UNSUPPORTED, "fork: too much for one launch; fewer layers or rows a call");
     if (c->pages_in_use + pages > c->pool_pages)
         return fail(HIKV_ERR_CAPACITY, "fork: page pool exhausted (%lld in use + %lld > %lld)", (long long)c->pages_in_use,
                     (long long)pages, (long long)c->pool_pages);

@@ -462,7 +462,8 @@ hikv_status hikv_accept(hikv_cache* cache, int32_t layer0, int32_t nlayers, cons
  * with no cut since; only the rows past them are copied (scores and positions all).
  * May be captured as hikv_append_packed.
  * Errors: INVALID_ARG (a row out of range, a copy of a copy, same_host above what
- * either unit holds), CAPACITY (the page pool), OUT_OF_MEMORY (host memory). */
+ * either unit holds), CAPACITY (the page pool), OUT_OF_MEMORY (host memory),
+ * UNSUPPORTED (more than 2^31 parts of 32 slots). */
 hikv_status hikv_fork(hikv_cache* cache, int32_t layer0, int32_t nlayers, const int32_t* src_host,
                       const int32_t* same_host, hikv_stream_t stream);
 
