@@ -426,8 +426,8 @@ class Cache:
         hikv_append(self.h, layer0, k, v, stream)
 
     def _counts(self, counts, name):
-        """HOST int32 [batch] (its address, its sum, what keeps it alive) from
-        a list, array or CPU tensor of whole numbers."""
+        """HOST int32 [batch] of the binding's own (its address, its sum, what
+        keeps it alive) from a list, array or CPU tensor of whole numbers."""
         batch = self.cfg.batch
         if type(counts) in (list, tuple) and len(counts) == batch and set(map(type, counts)) == {int}:
             try:
@@ -443,7 +443,7 @@ class Cache:
                 raise ValueError(f"{name} has shape {a.shape}, expected ({batch},)")
             if a.max() > 0x7FFFFFFF or a.min() < -1:
                 raise ValueError(f"{name} holds values out of range")
-            a = np.ascontiguousarray(a, dtype=np.int32)
+            a = np.array(a, dtype=np.int32, order="C")   # (a copy: a Tree keeps it)
             low, total, ptr = int(a.min()), int(a.sum(dtype=np.int64)), a.ctypes.data
         if low < -1:
             raise ValueError(f"{name} holds values out of range")
@@ -532,7 +532,7 @@ class Cache:
             with torch.cuda.stream(torch.cuda.ExternalStream(s, device=parent.device)):
                 mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
         _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
-        return Tree._made(keep, mask, depth, self.device_index, counts)
+        return Tree._made(tuple(keep.tolist()), mask, depth, self.device_index, counts)
 
     def _tree(self, tree, name, stream=None):
         """A Tree's counts and one of its tensors, checked against this cache."""

@@ -1,0 +1,86 @@
+"""The binding's own part of the window, tree and copy entry points, with the
+C calls and the device tensors stood in for: no device is needed."""
+import array
+import ctypes
+from types import SimpleNamespace
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_packed_api import cache, hk  # noqa: F401
+
+
+class DeviceTensor:
+    """What the binding asks of a CUDA tensor."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype, self.is_cuda, self.device = torch.Size(shape), dtype, True, "cuda:0"
+        self.streams = []
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def stride(self):
+        s = [1]
+        for n in reversed(self.shape[1:]):
+            s.insert(0, s[0] * n)
+        return tuple(s)
+
+    def new_empty(self, shape):
+        return DeviceTensor(*shape, dtype=self.dtype)
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+@pytest.fixture
+def calls(hk, cache, monkeypatch):
+    """Calls on a batch of two: the host counts that each C call reads, by name."""
+    read = {}
+
+    def c_call(name, at):
+        def call(*args):
+            read[name] = list((ctypes.c_int32 * 2).from_address(args[at]))
+            return hk.HIKV_OK
+        return call
+
+    where = {"hikv_tree_masks": 1, "hikv_append_tree": 2, "hikv_attend_tree": 2, "hikv_accept": 3}
+    monkeypatch.setattr(hk, "_lib", SimpleNamespace(**{n: c_call(n, at) for n, at in where.items()}))
+    monkeypatch.setattr(cache, "_int32", torch.int32, raising=False)
+    monkeypatch.setattr(cache, "_row_args", [hk.hikv_rows() for _ in range(4)], raising=False)
+    monkeypatch.setattr(cache, "_row_refs", [ctypes.byref(r) for r in cache._row_args], raising=False)
+    monkeypatch.setattr(cache, "_stream_int", lambda stream: stream or 0)
+    return read
+
+
+def in_int32(kind, values):
+    return {"array": lambda: np.array(values, dtype=np.int32), "tensor": lambda: torch.tensor(values, dtype=torch.int32),
+            "buffer": lambda: array.array("i", values), "list": lambda: list(values)}[kind]()
+
+
+@pytest.mark.parametrize("kind", ["array", "tensor", "buffer", "list"])
+def test_a_tree_has_counts_of_its_own(cache, calls, kind):
+    """The caller's counts are filled again for the next step while the tree lives."""
+    n = in_int32(kind, [3, 4])
+    tree = cache.tree(DeviceTensor(7, dtype=torch.int32), n)
+    assert calls["hikv_tree_masks"] == [3, 4]
+    n[0], n[1] = 12, 1
+    kv, q, out = DeviceTensor(7, 2, 64), DeviceTensor(7, 4, 64), DeviceTensor(7, 4, 64)
+    rope = SimpleNamespace(device_index=0, ref=None)
+    cache.append_tree(kv, kv, tree, rope, q=q, q_out=out)
+    cache.attend_tree(q, out, tree)
+    cache.accept(tree, [[0], [1, 3]])
+    assert calls == {name: [3, 4] for name in calls} and len(calls) == 4
+    assert list(tree.ntok) == [3, 4]
+    with pytest.raises(TypeError):   # (and what a tree says of itself is not what the calls read)
+        tree.ntok[0] = 12
