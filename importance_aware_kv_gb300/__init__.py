@@ -154,6 +154,12 @@ def _stream_of(t, stream):
     return _stream(None).value
 
 
+def _torch_stream(handle, device):
+    """torch's stream of a handle (0 as an external stream would be a new one of its pool)."""
+    import torch
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 def _ptr_checked(t, name, dtype, shape):
     """One pass of the checks _dev makes, returning the device pointer as an int."""
     if not t.is_cuda:
@@ -529,7 +535,7 @@ class Cache:
             mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
         else:   # memory of that stream's, so that no other one's work is still on it
             import torch
-            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=parent.device)):
+            with torch.cuda.stream(_torch_stream(s, parent.device)):
                 mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
         _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
         return Tree._made(tuple(keep.tolist()), mask, depth, self.device_index, counts)
@@ -547,8 +553,7 @@ class Cache:
         if t.shape[0] != total:
             raise ValueError(f"{name} has {t.shape[0]} rows, the tree {total} nodes")
         if stream is not None:   # (the tensor's memory is another stream's, perhaps)
-            import torch
-            t.record_stream(torch.cuda.ExternalStream(self._stream_int(stream), device=t.device))
+            t.record_stream(_torch_stream(self._stream_int(stream), t.device))
         return n, total, t.data_ptr()
 
     def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):

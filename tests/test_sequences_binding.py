@@ -84,3 +84,33 @@ def test_a_tree_has_counts_of_its_own(cache, calls, kind):
     assert list(tree.ntok) == [3, 4]
     with pytest.raises(TypeError):   # (and what a tree says of itself is not what the calls read)
         tree.ntok[0] = 12
+
+
+def test_the_default_stream_is_no_new_stream(hk, cache, calls, monkeypatch):
+    """Given by its handle, 0, which torch takes as "any stream" where it makes
+    one from a handle."""
+    used = []
+
+    def external(handle, device=None):
+        assert handle != 0
+        return handle
+
+    class On:
+        def __init__(self, stream):
+            used.append(stream)
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            pass
+
+    monkeypatch.setattr(cache, "_stream_int", lambda stream: 5 if stream is None else stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    tree = cache.tree(DeviceTensor(7, dtype=torch.int32), [3, 4], stream=0)
+    assert used == ["default"]
+    q, out = DeviceTensor(7, 4, 64), DeviceTensor(7, 4, 64)
+    cache.attend_tree(q, out, tree, stream=0)
+    assert set(tree.mask.streams) <= {"default"}
