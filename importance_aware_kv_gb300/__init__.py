@@ -228,13 +228,24 @@ class Tree:
         self.ntok, self.mask, self.depth = tuple(getattr(ntok, "tolist", lambda: ntok)()), mask, depth
         self.device_index = mask.device.index
         self.counts = None   # ntok as the C ABI takes it, once a cache has checked it
+        self.streams = set()   # handles of the streams that the tensors' memory waits for
 
     @classmethod
-    def _made(cls, ntok, mask, depth, device_index, counts):
-        """One whose tensors and counts a cache has made itself."""
+    def _made(cls, ntok, mask, depth, device_index, counts, stream):
+        """One whose tensors and counts a cache has made itself, on that stream."""
         t = cls.__new__(cls)
         t.ntok, t.mask, t.depth, t.device_index, t.counts = ntok, mask, depth, device_index, counts
+        t.streams = {stream}
         return t
+
+    def _hold(self, stream):
+        """Before a call on the stream: its use of the tensors is known to the allocator."""
+        if stream not in self.streams:
+            s = _torch_stream(stream, self.mask.device)
+            for t in (self.mask, self.depth):
+                if t is not None:
+                    t.record_stream(s)
+            self.streams.add(stream)
 
 
 class _DeviceArray:
@@ -538,9 +549,9 @@ class Cache:
             with torch.cuda.stream(_torch_stream(s, parent.device)):
                 mask, depth = parent.new_empty((total, words)), parent.new_empty((total,))
         _check(_lib.hikv_tree_masks(self.h, n, parent.data_ptr(), mask.data_ptr(), words, depth.data_ptr(), s))
-        return Tree._made(tuple(keep.tolist()), mask, depth, self.device_index, counts)
+        return Tree._made(tuple(keep.tolist()), mask, depth, self.device_index, counts, s)
 
-    def _tree(self, tree, name, stream=None):
+    def _tree(self, tree, name):
         """A Tree's counts and one of its tensors, checked against this cache."""
         if tree.device_index != self.device_index:
             raise ValueError(f"the tree is on {tree.mask.device}, the cache on cuda:{self.device_index}")
@@ -552,15 +563,13 @@ class Cache:
             raise ValueError(f"the tree has no {name}")
         if t.shape[0] != total:
             raise ValueError(f"{name} has {t.shape[0]} rows, the tree {total} nodes")
-        if stream is not None:   # (the tensor's memory is another stream's, perhaps)
-            t.record_stream(_torch_stream(self._stream_int(stream), t.device))
         return n, total, t.data_ptr()
 
     def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):
         """append_packed of a Tree's nodes, k (and q) rotated by the position of
         the sequence's first node plus the node's depth."""
         c = self.cfg
-        n, total, depth = self._tree(tree, "depth", stream)
+        n, total, depth = self._tree(tree, "depth")
         rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
@@ -569,16 +578,20 @@ class Cache:
             rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, q_out, "q_out", total, c.num_q_heads)
         if rope.device_index != self.device_index:
             raise ValueError(f"rope is on {rope.cos.device}, the cache on cuda:{self.device_index}")
-        _check(_lib.hikv_append_tree(self.h, layer, n, depth, rk, rv, rq, ro, rope.ref, self._stream_int(stream)))
+        s = self._stream_int(stream)
+        tree._hold(s)
+        _check(_lib.hikv_append_tree(self.h, layer, n, depth, rk, rv, rq, ro, rope.ref, s))
 
     def attend_tree(self, q, out, tree, layer=0, stream=None):
         """Attention of the newest tree.ntok[b] tokens of every sequence over
         everything in front of them and, among themselves, what the tree's masks
         say: q, out [sum ntok][Hq][d] as for attend_packed."""
         c = self.cfg
-        n, total, mask = self._tree(tree, "mask", stream)
+        n, total, mask = self._tree(tree, "mask")
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
-        _check(_lib.hikv_attend_tree(self.h, layer, n, mask, tree.mask.shape[1], rq, ro, self._stream_int(stream)))
+        s = self._stream_int(stream)
+        tree._hold(s)
+        _check(_lib.hikv_attend_tree(self.h, layer, n, mask, tree.mask.shape[1], rq, ro, s))
 
     def accept(self, ntree, accepted, layer0=0, nlayers=None, stream=None):
         """Keep, of the newest ntree[b] tokens of batch row b, those that the

@@ -114,3 +114,30 @@ def test_the_default_stream_is_no_new_stream(hk, cache, calls, monkeypatch):
     q, out = DeviceTensor(7, 4, 64), DeviceTensor(7, 4, 64)
     cache.attend_tree(q, out, tree, stream=0)
     assert set(tree.mask.streams) <= {"default"}
+
+
+def test_a_tree_is_held_for_every_stream_that_uses_it(hk, cache, calls, monkeypatch):
+    """Its tensors are memory of the stream it was made on: any other one's use
+    of them, given by handle or the current one, is known to the allocator."""
+    current = [7]
+    monkeypatch.setattr(cache, "_stream_int", lambda stream: current[0] if stream is None else stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: s)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    tree = cache.tree(DeviceTensor(7, dtype=torch.int32), [3, 4])
+    kv, q, out = DeviceTensor(7, 2, 64), DeviceTensor(7, 4, 64), DeviceTensor(7, 4, 64)
+    rope = SimpleNamespace(device_index=0, ref=None)
+
+    def use(stream=None):
+        cache.append_tree(kv, kv, tree, rope, q=q, q_out=out, stream=stream)
+        cache.attend_tree(q, out, tree, stream=stream)
+
+    use()
+    use(7)
+    assert set(tree.mask.streams) <= {7} and set(tree.depth.streams) <= {7}
+    use(9)
+    current[0] = 11
+    use()
+    current[0] = 0
+    use()
+    for t in (tree.mask, tree.depth):
+        assert set(t.streams) - {7} == {9, 11, 0}
