@@ -525,8 +525,14 @@ class Cache:
         if isinstance(window, (int, np.integer)) and not isinstance(window, bool):
             window = [window] * c.num_kv_heads
         w = self._ints(window, "window", c.num_kv_heads)
+        if type(sink) is not int:
+            a = np.asarray(sink)
+            if a.ndim or a.dtype.kind not in "iu":
+                raise TypeError("sink must be a whole number")
+            sink = int(a)
+        if not -1 << 31 <= sink < 1 << 31:
+            raise ValueError("sink is out of range")
         rq, ro = self._rows(2, q, "q", total, c.num_q_heads), self._rows(3, out, "out", total, c.num_q_heads)
-        sink = min(max(int(sink), -1), 0x7FFFFFFF)
         _check(_lib.hikv_attend_window(self.h, layer, n, w.buffer_info()[0], sink, rq, ro, self._stream_int(stream)))
 
     def tree(self, parent, ntok, stream=None):

@@ -141,3 +141,17 @@ def test_a_tree_is_held_for_every_stream_that_uses_it(hk, cache, calls, monkeypa
     use()
     for t in (tree.mask, tree.depth):
         assert set(t.streams) - {7} == {9, 11, 0}
+
+
+def test_sink_is_a_whole_number(cache):
+    """Checked as the windows are, before the tensors."""
+    x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    for bad in (3.9, "4", True, None, [4], np.float32(4), np.bool_(True)):
+        with pytest.raises(TypeError, match="sink"):
+            cache.attend_window(x, x, [1, 2], 4, sink=bad)
+    for bad in (1 << 31, 1 << 63, -(1 << 31) - 1, np.int64(1 << 40)):
+        with pytest.raises(ValueError, match="sink"):
+            cache.attend_window(x, x, [1, 2], 4, sink=bad)
+    for good in (0, 4, np.int32(4), np.uint8(4), 0x7FFFFFFF, torch.tensor(4)):   # (as far as the host tensors)
+        with pytest.raises(TypeError, match="CUDA"):
+            cache.attend_window(x, x, [1, 2], 4, sink=good)
