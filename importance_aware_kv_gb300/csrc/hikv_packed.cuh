@@ -316,6 +316,14 @@ struct RowSight<TreeMask> {
         const uint32_t lo = at(i);
         return b & 31 ? __funnelshift_r(lo, at(i + 1), b & 31) : lo;
     }
+    // (rare) Whether the row sees nothing.  A sum of weights of zero does not say so:
+    // the logits of what it sees can all be -inf.
+    __device__ __forceinline__ bool blind() const {
+        if (seen0 > 0) return false;
+        for (int32_t i = 0; 32 * i < nq; ++i)
+            if (at(i)) return false;
+        return true;
+    }
 };
 
 cudaError_t launch_attend_tc(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap, int d,

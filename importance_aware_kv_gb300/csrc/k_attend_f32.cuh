@@ -368,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool wide = splits > 1 || (((uintptr_t)a.out.p | a.out.ts | a.out.hs) & 31) == 0;
             float inv = splits > 1 ? 1.f : 1.0f / l;
-            if (M::kind == 2 && splits == 1 && l == 0.f) inv = 0.f;   // a row that sees nothing
+            if constexpr (M::kind == 2) {
+                if (splits == 1 && l == 0.f &&
+                    RowSight<M>(mask, g, first + (min(row, rows - 1) >> a.gshift), seen0, nq, lim).blind())
+                    inv = 0.f;   // (the sums are zero)
+            }
             const int32_t row4 = row & ~3;
             const int32_t pt = M::kind != 0 ? part_token(a, i) : 0;   // of a token in the partial results, from its packed row
             uint8_t* dst[4];   // lane k of each four writes the k-th 32 bytes of four rows' 128

@@ -57,9 +57,12 @@ __global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ Att
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
     if (gave_up) return;
+    if constexpr (M::kind == 2) {
+        if (l == 0.f && RowSight<M>(mask, h >> a.gshift, a.start[i] + j, n - a.nq[i], a.nq[i], lim).blind()) l = 1.f;   // (o is zero)
+    }
     T* dst = reinterpret_cast<T*>(a.out.row(a.start[i] + j, h)) + lane * E;
 #pragma unroll
-    for (int k = 0; k < E; ++k) dst[k] = Elem<T>::from_f(M::kind == 2 && l == 0.f ? 0.f : o[k] / l);
+    for (int k = 0; k < E; ++k) dst[k] = Elem<T>::from_f(o[k] / l);
 }
 
 template <class M>

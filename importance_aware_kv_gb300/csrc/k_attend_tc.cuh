@@ -64,6 +64,8 @@
 // an item change costs 2.5 us, two steps.
 #pragma once
 
+#include <cfloat>
+
 #include "hikv_tcgen05.cuh"
 
 namespace hikv {
@@ -391,12 +393,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else if (M::kind == 2 ? s0 + kKeys - 1 > w.lim0
                                         : s0 + kKeys - 1 > lim_w || (s0 < from_w && s0 + kKeys - 1 >= mask_sink)) {
+                    uint32_t any = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t sees = sight().word(s0 + 32 * k);
+                        any |= sees;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) s[32 * k + j] = (sees >> j) & 1 ? s[32 * k + j] : 0xFF800000u;
                     }
+                    // (trees: a row that has seen something, if only logits of -inf, no longer has top = -inf)
+                    if (M::kind == 2 && any) top = fmaxf(top, -FLT_MAX);
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
@@ -423,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     settle();
                     l *= f;
-                    top = m = mt;
+                    if (M::kind != 2 || mt != -INFINITY) top = mt;
+                    m = mt;
                 }
                 top = fmaxf(top, mt);
                 const float base = reference();
@@ -454,7 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             settle();
             if (nt > 0) {
                 float inv = w.split < 0 ? 1.0f / l : 1.f;
-                if (M::kind == 2 && w.split < 0 && l == 0.f) inv = 0.f;   // a row that sees nothing
+                // a row that sees nothing (O is zero).  l = 0 alone would not say so.
+                if (M::kind == 2 && w.split < 0 && w.seen0 == 0 && top == -INFINITY) inv = 0.f;
                 // lane i of each four ends up with the i-th 32 bytes of four rows' 128
                 const int32_t row4 = row & ~3;
                 int32_t pt = 0;   // of a token in the partial results, from its packed row

@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_packed import DEV, gen_of, hk, make, rnd, tables  # noqa: F401
-from tests.test_gpu_sequences import check, fill, paths_of, queries, random_tree, tree_sees
+from tests.test_gpu_packed import DEV, DT, gen_of, hk, make, rnd, tables  # noqa: F401
+from tests.test_gpu_sequences import bits_of, check, fill, paths_of, queries, random_tree, tree_sees
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,100 @@ def test_a_tree_made_before_a_capture(hk):
     del graph, tree
     torch.cuda.synchronize()
     check(cache, q, eager, new, sees)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("held", [0, 130, 9000])
+def test_logits_of_minus_infinity_are_seen(hk, dtype, held):
+    """A row all of whose seen logits overflow to -inf has no softmax (0 / 0), in a
+    tree as in the other calls; one that sees nothing is zero; the others are
+    what they are without it."""
+    n, g = 70, gen_of(65)
+    cache = make(hk, 1, 8, 1, 64, dtype, held + n)
+    low = torch.full((max(held, n), 1, 64), -3e38, device=DEV, dtype=DT[dtype])
+    v = rnd(g, held + n, 1, 64, dtype=dtype)
+    if held:
+        cache.append_packed(low[:held], v[:held], [held])
+    cache.append_packed(low[:n], v[held:], [n])
+    q = torch.zeros(n, 8, 64, device=DEV, dtype=DT[dtype])
+    q[7], q[33:36], q[69] = 3e38, 3e38, 3e38
+    m = torch.eye(n, dtype=torch.bool)
+    m[34] = False          # sees nothing but what is in front
+    m[40] = False
+    tree = hk.Tree([n], bits_of(m, 3).to(DEV))
+    out = torch.full_like(q, 7.0)
+    before = cache.kernel_launches()
+    cache.attend_tree(q, out, tree)
+    assert held < 9000 or cache.kernel_launches() - before == 2
+    causal, window = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    cache.attend_packed(q, causal, [n])
+    cache.attend_window(q, window, [n], 1)
+    lost = torch.zeros(n, dtype=torch.bool, device=DEV)
+    lost[[7, 33, 34, 35, 69]] = True
+    for x in (causal, window):
+        assert bool(torch.isnan(x[lost]).all()) and bool(torch.isfinite(x[~lost]).all())
+    if held == 0:
+        assert bool((out[[34, 40]] == 0).all())
+        lost[34] = False
+    assert bool(torch.isnan(out[lost]).all()) and bool(torch.isfinite(out[~lost]).all())
+    # equal logits: the mean of what is seen
+    k = torch.cat([torch.ones(n, held, dtype=torch.bool), m], 1).double().to(DEV)
+    mean = (k @ v[:, 0].double()) / k.sum(1, keepdim=True).clamp_min(1)
+    size = (k @ v[:, 0].double().abs()) / k.sum(1, keepdim=True).clamp_min(1)
+    h = torch.finfo(DT[dtype]).eps / 2
+    tol = (2 * (held + n) * 2.0 ** -24 + 8 * 2.0 ** -24 + (h if dtype == "bf16" else 0)) * size + h * mean.abs()
+    err = (out.double() - mean[:, None]).abs()
+    assert bool((err <= tol[:, None])[~lost].all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_split_rows_that_see_nothing(hk, dtype):
+    """Nothing in front of a long tree whose keys are split over work items."""
+    n, gen, cpu = 1900, gen_of(66), torch.Generator().manual_seed(66)
+    cache = make(hk, 1, 2, 1, 64, dtype, n)
+    fill(cache, gen, [[n]])
+    m = torch.rand(n, n, generator=cpu) < 0.01
+    m[:, 300:600] = False
+    m[[0, 5, 127, 128, 1000, n - 1]] = False
+    m[77], m[78] = False, False
+    m[77, n - 1] = m[78, 0] = True      # one key each, in the last and the first part
+    tree = hk.Tree([n], bits_of(m, 60).to(DEV))
+    q, out = queries(cache, gen, n)
+    before = cache.kernel_launches()
+    cache.attend_tree(q, out, tree)
+    assert cache.kernel_launches() - before == 2
+    check(cache, q, out, [n], tree_sees([m], [0]))
+    blind = ~m.any(1).to(DEV)
+    assert int(blind.sum()) >= 6 and bool((out[blind] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_minus_infinity_in_front_of_larger_logits(hk, dtype):
+    """Rows whose only logit is -inf, in the first tile of keys, between rows
+    whose maximum moves in every later one."""
+    n, g = 400, gen_of(67)
+    cache = make(hk, 1, 2, 1, 64, dtype, n)
+    k = torch.zeros(n, 1, 64, device=DEV, dtype=DT[dtype])
+    k[:128] = -3e38
+    k[128:, 0, 0] = 10.0 * torch.arange(n - 128, device=DEV)
+    v = rnd(g, n, 1, 64, dtype=dtype)
+    cache.append_packed(k, v, [n])
+    m = torch.zeros(n, n, dtype=torch.bool)
+    m[:, 128:] = True
+    odd = torch.arange(1, n, 2)
+    m[odd] = False
+    m[odd, odd % 128] = True
+    m[7] = False
+    tree = hk.Tree([n], bits_of(m, 13).to(DEV))
+    q = torch.zeros(n, 2, 64, device=DEV, dtype=DT[dtype])
+    q[:, :, 0] = 1.0
+    plain, out = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    tame = q.clone()
+    tame[odd] = 0.0
+    cache.attend_tree(tame, plain, tree)
+    check(cache, tame, plain, [n], tree_sees([m], [0]))
+    q[odd] = 3e38
+    cache.attend_tree(q, out, tree)
+    assert torch.equal(out[::2], plain[::2]) and bool((out[7] == 0).all())
+    lost = odd[odd != 7].to(DEV)
+    assert bool(torch.isnan(out[lost]).all())
