@@ -48,7 +48,9 @@ hikv_status fail(hikv_status s, const char* fmt, ...) {
     return s;
 }
 
+// (the runtime's note of the error goes with it: a later launch would find it and take it for its own)
 hikv_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();
     return fail(HIKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

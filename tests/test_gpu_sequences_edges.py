@@ -1,11 +1,13 @@
 """GPU tests of the window, tree and copy entry points where a caller's
 buffers, streams or heads differ from the plain case.  Results against 64 bits
 with the tolerances of tests/test_gpu_sequences.py."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_packed import DEV, DT, gen_of, hk, make, rnd, tables  # noqa: F401
+from tests.test_gpu_packed import DEV, DT, gen_of, hk, make, rnd, slots, tables  # noqa: F401
 from tests.test_gpu_sequences import bits_of, check, fill, paths_of, queries, random_tree, tree_sees
 
 pytestmark = pytest.mark.gpu
@@ -210,3 +212,43 @@ def test_minus_infinity_in_front_of_larger_logits(hk, dtype):
     assert torch.equal(out[::2], plain[::2]) and bool((out[7] == 0).all())
     lost = odd[odd != 7].to(DEV)
     assert bool(torch.isnan(out[lost]).all())
+
+
+class Refused:
+    """While this lasts nothing can be launched on the default stream: a stream
+    that it waits for is being captured.  A host error, no work on the device."""
+
+    def __enter__(self):
+        self.cu, self.s = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+        assert self.cu.cuStreamCreate(ctypes.byref(self.s), 0) == 0
+        assert self.cu.cuStreamBeginCapture_v2(self.s, 2) == 0
+
+    def __exit__(self, *a):
+        graph = ctypes.c_void_p()
+        self.cu.cuStreamEndCapture(self.s, ctypes.byref(graph))   # (an error: the capture is lost)
+        if graph.value:
+            self.cu.cuGraphDestroy(graph)
+        assert self.cu.cuStreamDestroy_v2(self.s) == 0
+
+
+def test_a_failed_launch_is_not_the_next_calls_error(hk):
+    """The next call, of another kind, is carried out and says so."""
+    cfg = dict(budgets=[24, 30], num_sink=2, recent_window=8)
+    cache, other = (make(hk, 2, 4, 2, 64, "bf16", 128, **cfg) for _ in range(2))
+    new = [40, 33]
+    for c in (cache, other):
+        fill(c, gen_of(69), [new])
+    q, out = queries(cache, gen_of(69), sum(new))
+    torch.cuda.synchronize()
+    for call in (lambda c: c.evict(), lambda c: c.append(*(torch.ones(1, 2, 2, 3, 64, device=DEV, dtype=torch.bfloat16),) * 2),
+                 lambda c: c.decode_step(q[None, :2].contiguous(), out[None, :2].contiguous()), lambda c: c.evict(),
+                 lambda c: c.drop()):
+        with Refused(), pytest.raises(hk.HikvError, match="fork: launch") as e:
+            cache.fork([0, 0])
+        assert e.value.status == hk.HIKV_ERR_CUDA
+        call(cache)
+        call(other)
+        assert cache.lengths().tolist() == other.lengths().tolist()
+        for u in range(4):
+            assert all(torch.equal(x, y) for x, y in zip(slots(cache, u), slots(other, u)))
+    cache.device_status()
