@@ -107,6 +107,7 @@ struct NvtxRange {
 // Set hikv_last_error() and return `s`.
 hikv_status fail(hikv_status s, const char* fmt, ...);
 hikv_status cuda_fail(cudaError_t e, const char* what);
+hikv_status cuda_fail(cudaError_t e, const char* who, const char* part);
 void set_last_error(const char* msg);
 
 // cuTensorMapEncodeTiled from the driver, or null.

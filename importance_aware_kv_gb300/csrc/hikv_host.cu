@@ -53,6 +53,10 @@ hikv_status cuda_fail(cudaError_t e, const char* what) {
     cudaGetLastError();
     return fail(HIKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+hikv_status cuda_fail(cudaError_t e, const char* who, const char* part) {
+    cudaGetLastError();
+    return fail(HIKV_ERR_CUDA, "%s: %s: %s", who, part, cudaGetErrorString(e));
+}
 
 // cuTensorMapEncodeTiled from the driver, found through the runtime (no
 // link-time dependency on libcuda).

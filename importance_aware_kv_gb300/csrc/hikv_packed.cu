@@ -271,7 +271,7 @@ cudaError_t launch_join(const hikv_cache* c, const Sees& sees, const AttendArgs&
 hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t total, const hikv_rows* q,
                           const hikv_rows* out, Sees& sees, hikv_stream_t stream, const char* who) {
     DeviceGuard guard(c->device);
-    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who, "device");
     pdl_forget(c);
     const bool bf16 = c->dtype == HIKV_BF16;
     sees.window.align = bf16 ? std::min(c->P, 128) : 1;   // rows of a box of the tensor map of the pages
@@ -352,7 +352,7 @@ hikv_status attend_launch(hikv_cache* c, int u0, const int32_t* nq, int64_t tota
             e = launch_join(c, sees, a, (cudaStream_t)stream);
             c->launches += 1;
         }
-        if (e != cudaSuccess) return cuda_fail(e, who);
+        if (e != cudaSuccess) return cuda_fail(e, who, "launch");
     }
     return HIKV_OK;
 }
@@ -456,7 +456,7 @@ hikv_status append_rows(hikv_cache* c, int32_t layer, const int32_t* ntok, bool 
         return fail(HIKV_ERR_CAPACITY, "%s: page pool exhausted (%lld in use + %lld > %lld)", who,
                     (long long)c->pages_in_use, (long long)new_pages, (long long)c->pool_pages);
     DeviceGuard guard(c->device);
-    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who);
+    if (guard.status != cudaSuccess) return cuda_fail(guard.status, who, "device");
     pdl_forget(c);
     PackedAppendArgs a{};
     a.v = c->v;
@@ -498,7 +498,7 @@ hikv_status append_rows(hikv_cache* c, int32_t layer, const int32_t* ntok, bool 
         a.reserved = known ? nullptr : c->d_append_base;
         cudaError_t e = launch_append_packed(a, c->dtype, c->sm_count, (cudaStream_t)stream);
         c->launches += known ? 1 : 2;
-        if (e != cudaSuccess) return cuda_fail(e, who);
+        if (e != cudaSuccess) return cuda_fail(e, who, "launch");
         for (int i = 0; i < n; ++i) {
             const int m = ntok[b0 + i], ub = u0 + (b0 + i) * Hkv;
             if (m == 0) continue;

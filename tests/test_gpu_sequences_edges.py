@@ -252,3 +252,35 @@ def test_a_failed_launch_is_not_the_next_calls_error(hk):
         for u in range(4):
             assert all(torch.equal(x, y) for x, y in zip(slots(cache, u), slots(other, u)))
     cache.device_status()
+
+
+def test_a_failed_launch_says_which_call_and_that_it_was_the_launch(hk):
+    """And leaves the cache as it was."""
+    cache = make(hk, 2, 4, 2, 64, "bf16", 128)
+    gen, new = gen_of(68), [5, 3]
+    fill(cache, gen, [[20, 9], new])
+    parent = torch.tensor([-1, 0, 0, 1, 1, -1, 0, 0], dtype=torch.int32, device=DEV)
+    tree, rope = cache.tree(parent, new), hk.Rope(*tables(128, 64))
+    k, v = (rnd(gen, 8, 2, 64, dtype="bf16") for _ in range(2))
+    q, out = queries(cache, gen, 8)
+    torch.cuda.synchronize()
+    want = cache.lengths().tolist()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    for name, call in (("append_packed", lambda: cache.append_packed(k, v, new)),
+                       ("attend_packed", lambda: cache.attend_packed(q, out, new)),
+                       ("attend_window", lambda: cache.attend_window(q, out, new, 4)),
+                       ("tree_masks", lambda: cache.tree(parent, new)),
+                       ("append_tree", lambda: cache.append_tree(k, v, tree, rope)),
+                       ("attend_tree", lambda: cache.attend_tree(q, out, tree)),
+                       ("accept", lambda: cache.accept(tree, [[0, 1], [0]])),
+                       ("fork", lambda: cache.fork([0, 0])),
+                       ("drop", lambda: cache.drop([1, 1]))):
+        with Refused(), pytest.raises(hk.HikvError, match=name + ": launch") as e:
+            call()
+        assert e.value.status == hk.HIKV_ERR_CUDA
+        assert cache.lengths().tolist() == want
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+    cache.attend_tree(q, out, tree)
+    check(cache, q, out, new, tree_sees([paths_of([-1, 0, 0, 1, 1]), paths_of([-1, 0, 0])], [20, 9]))
+    cache.device_status()
