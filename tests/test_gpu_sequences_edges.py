@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from tests.test_gpu_packed import DEV, DT, gen_of, hk, make, rnd, slots, tables  # noqa: F401
-from tests.test_gpu_sequences import bits_of, check, fill, paths_of, queries, random_tree, tree_sees
+from tests.test_gpu_sequences import (bits_of, check, fill, paths_of, queries, random_tree, tree_sees,
+                                      window_sees)
 
 pytestmark = pytest.mark.gpu
 
@@ -283,4 +284,60 @@ def test_a_failed_launch_says_which_call_and_that_it_was_the_launch(hk):
     assert bool((out == 7.0).all())
     cache.attend_tree(q, out, tree)
     check(cache, q, out, new, tree_sees([paths_of([-1, 0, 0, 1, 1]), paths_of([-1, 0, 0])], [20, 9]))
+    cache.device_status()
+
+
+# Cut caches: budgets per head, tokens appended since; few queries, so that the
+# keys are split over work items
+UNEVEN = [("bf16", 128, 8, [6000, 700]), ("bf16", 64, 2, [3100, 40, 5000]), ("f32", 64, 4, [6000, 700]),
+          ("f32", 128, 8, [129, 4000])]
+
+
+def uneven(hk, dtype, d, group, budgets, held, since, new, gen):
+    cache = make(hk, len(held), group * len(budgets), len(budgets), d, dtype, max(map(sum, zip(held, since, new))),
+                 budgets=budgets, num_sink=4, recent_window=16)
+    fill(cache, gen, [held])
+    cache.evict()
+    fill(cache, gen, [since, new])
+    n = cache.lengths().reshape(len(held), -1)
+    assert any(len(set(row)) > 1 for row in n.tolist())
+    return cache
+
+
+@pytest.mark.parametrize("dtype,d,group,budgets", UNEVEN)
+@pytest.mark.parametrize("new", [[1], [5, 3], [37, 0, 1]])
+def test_tree_split_over_heads_of_unequal_length(hk, dtype, d, group, budgets, new):
+    gen, cpu = gen_of(62 + sum(new)), torch.Generator().manual_seed(62)
+    held, since = [7000, 900, 6500][:len(new)], [0, 77, 300][:len(new)]
+    cache = uneven(hk, dtype, d, group, budgets, held, since, new, gen)
+    masks = [torch.rand(n, n, generator=cpu) < 0.5 for n in new]
+    tree = hk.Tree(new, torch.cat([bits_of(m, 2) for m in masks]).to(DEV))
+    q, out = queries(cache, gen, sum(new))
+    before = cache.kernel_launches()
+    cache.attend_tree(q, out, tree)
+    assert cache.kernel_launches() - before == 2
+    check(cache, q, out, new, tree_sees(masks, held))
+    before = cache.kernel_launches()
+    cache.attend_packed(q, out, new)
+    assert cache.kernel_launches() - before == 2
+    check(cache, q, out, new, lambda b, g, n, pos: pos[None] <= int(pos.max()) - new[b] + 1
+          + torch.arange(new[b], device=DEV)[:, None])
+    cache.device_status()
+
+
+@pytest.mark.parametrize("dtype,d,group,budgets", UNEVEN)
+@pytest.mark.parametrize("new", [[1], [5, 3], [37, 0, 1]])
+def test_window_split_over_heads_of_unequal_length(hk, dtype, d, group, budgets, new):
+    """A window for every head inside what was appended since the cut; head 0
+    sees all that it holds."""
+    gen = gen_of(63 + sum(new))
+    held, since = [7000, 900, 6500][:len(new)], [2600, 2500, 2700][:len(new)]
+    cache = uneven(hk, dtype, d, group, budgets, held, since, new, gen)
+    for windows, sink in (([0, 2400, 1100], 4), ([2400, 2400, 2400], 0), ([1500, 0, 7], 3)):
+        windows = windows[:len(budgets)]
+        q, out = queries(cache, gen, sum(new))
+        before = cache.kernel_launches()
+        cache.attend_window(q, out, new, windows, sink)
+        assert cache.kernel_launches() - before == 2
+        check(cache, q, out, new, window_sees(new, windows, sink))
     cache.device_status()
