@@ -183,9 +183,11 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
     c->units = (int)units64;
     c->per_layer = c->B * c->Hkv;
     c->pool_pages = f.pool_pages ? f.pool_pages : (int64_t)c->units * c->max_pages;
-    if (c->pool_pages > INT32_MAX) {
+    const int64_t pages = c->pool_pages;
+    // (page ids, and the pool's rows as coordinates of tensor copies, are int32)
+    if (c->pool_pages > INT32_MAX / 2 / P) {
         delete c;
-        return fail(HIKV_ERR_UNSUPPORTED, "create: pool of %lld pages too large", (long long)f.pool_pages);
+        return fail(HIKV_ERR_UNSUPPORTED, "create: pool of %lld pages too large", (long long)pages);
     }
     c->scale = f.scale > 0.f ? f.scale : 1.0f / std::sqrt((float)c->d);
     c->pool_k = f.pool_kernel;
@@ -298,11 +300,10 @@ hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out) {
     {
         const uint64_t rows = (uint64_t)c->pool_pages * 2 * P;
         auto enc = tensor_map_encoder();
-        if (!enc || rows > 0xFFFFFFFFull) {
+        if (!enc) {
             free_all(c);
             delete c;
-            return fail(enc ? HIKV_ERR_UNSUPPORTED : HIKV_ERR_CUDA,
-                        enc ? "create: pool too large for one tensor map" : "create: cuTensorMapEncodeTiled unavailable");
+            return fail(HIKV_ERR_CUDA, "create: cuTensorMapEncodeTiled unavailable");
         }
         cuuint64_t dims[2] = {(cuuint64_t)c->d, (cuuint64_t)rows};
         cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
