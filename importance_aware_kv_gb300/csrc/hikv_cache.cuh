@@ -116,7 +116,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 inline void pdl_forget(hikv_cache* c) { if (c) c->pdl_valid = false; }
 
 inline bool range_ok(const hikv_cache* c, int32_t layer0, int32_t nl) {
-    return c && layer0 >= 0 && nl > 0 && layer0 + nl <= c->L;
+    return c && layer0 >= 0 && layer0 < c->L && nl > 0 && nl <= c->L - layer0;   // (their sum can pass 32 bits)
 }
 
 // The cache's device made current for the length of a call.

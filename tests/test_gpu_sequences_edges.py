@@ -341,3 +341,17 @@ def test_window_split_over_heads_of_unequal_length(hk, dtype, d, group, budgets,
         assert cache.kernel_launches() - before == 2
         check(cache, q, out, new, window_sees(new, windows, sink))
     cache.device_status()
+
+
+@pytest.mark.parametrize("layer0,nlayers", [(1, 0x7FFFFFFF), (0x7FFFFFFF, 1), (2, 1), (0, 3), (-1, 1), (1, 0), (1, -1)])
+def test_layers_out_of_range_are_refused(hk, layer0, nlayers):
+    """Their sum past 32 bits among them."""
+    cache = make(hk, 2, 4, 2, 64, "bf16", 64, layers=2)
+    fill(cache, gen_of(70), [[9, 5]])
+    at = dict(layer0=layer0, nlayers=nlayers)
+    for call in (lambda: cache.drop([1, 1], **at), lambda: cache.accept([2, 1], [[0], [0]], **at),
+                 lambda: cache.fork([0, 0], **at), lambda: cache.evict(**at)):
+        with pytest.raises(hk.HikvError) as e:
+            call()
+        assert e.value.status == hk.HIKV_ERR_INVALID_ARG
+    assert cache.lengths().tolist() == [9, 9, 5, 5, 0, 0, 0, 0]
