@@ -214,7 +214,8 @@ class Tree:
     Cache.append_tree: ntok[b] nodes of sequence b, mask [sum ntok][words] int32
     (bit j % 32 of word j / 32: the node sees node j of its sequence), depth
     [sum ntok] int32 (append_tree only).  Cache.tree makes one from parents; masks
-    of any shape can be given here.  Keeps a copy of ntok, and the tensors alive."""
+    of any shape can be given here.  Keeps a copy of ntok, and the tensors alive,
+    their memory for every stream of a call that used them."""
 
     def __init__(self, ntok, mask, depth=None):
         import torch
@@ -573,7 +574,8 @@ class Cache:
 
     def append_tree(self, k, v, tree, rope, layer=0, q=None, q_out=None, stream=None):
         """append_packed of a Tree's nodes, k (and q) rotated by the position of
-        the sequence's first node plus the node's depth."""
+        the sequence's first node plus the node's depth.  The tables reach the
+        sequence's nodes in a row, as for append_packed."""
         c = self.cfg
         n, total, depth = self._tree(tree, "depth")
         rk, rv = self._rows(0, k, "k", total, c.num_kv_heads), self._rows(1, v, "v", total, c.num_kv_heads)

@@ -187,6 +187,8 @@ double rounds(const std::vector<std::pair<double, int64_t>>& items, int64_t slot
 // single tokens in windows of 2044 (512 items of 17 steps, 32/8 heads): 99.5 us, all
 // whole 104.  With 256 rows an item partial results cost what it gains (60 tree nodes of
 // twelve sequences, 192 items, 64/8 heads: 53 us whole, 60 split).
+// (A model of cost alone: heads count as long as the sequence's longest, an item of
+// one row tile as one of two.)
 // Returns how many of the first sequences stay whole, *chunk keys per split of
 // the others; all of them and INT32_MAX where that does not pay.
 int attend_tail(const hikv_cache* c, const ItemShape& k, const Sees& sees, const AttendSeq* sq, int nseq, int32_t* chunk) {

@@ -57,9 +57,10 @@
 // masked by a word of bits for each 32 keys of a row, worked out by the row's
 // own thread; the keys between the first tokens and an item's window are left
 // out of its key numbers, so that they cost neither a load nor a product.
-// Measured: 64 tree nodes over eight 8K-32K caches 140 us (5.2 TB/s); a 16K prompt
-// in windows of 1024, 32/8 heads, 206 us (1.30 PFLOP/s of what is seen); one token
-// of 64 sequences in windows of 2044 98 us (5.5 TB/s).  A mask costs 600 to 1,000
+// Measured: 64 tree nodes over eight 8K-32K caches 140 to 162 us, by box (4.5 to 5.2
+// TB/s); a 16K prompt in windows of 1024, 32/8 heads, 206 to 226 us (1.18 to 1.30
+// PFLOP/s of what is seen); one token of 64 sequences in windows of 2044 98 us (5.5
+// TB/s).  A mask costs 600 to 1,000
 // cycles a tile, so a warp applies it only where its own rows do not all see the tile;
 // an item change costs 2.5 us, two steps.
 #pragma once
@@ -598,8 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) hand_out(w);
         while (ok && w.some) {
             Item next;
-            // The next item is asked for late, so that a CTA with a long item does not hold
-            // another one meanwhile, and read and handed out before it is loaded.
+            // Windows and trees: the next item is asked for late, so that a CTA with a long item
+            // does not hold another one meanwhile, and read and handed out before it is loaded.
+            // Asked for and read 14 and 10 fills before the end: five prompts of windows and
+            // retrieval heads 73.5 us, 64 single tokens in windows 98.7, trees of 33 to 61 nodes
+            // 53.3; early, as for causal attention, 77.1, 100.3 and 54.2; 24 and 20 before the
+            // end 77.9, 98.9 and 52.4; 8 and 4 72.5, 98.1 and 53.3, a 16K prompt then 226 (225).
             const int32_t fills = 2 * w.ntiles, when = M::kind == 0 ? min(4, fills) : min(fills, max(4, fills - 10));
             const int32_t ask_at = max(1, fills - 14);
             for (int32_t x = 0; ok && x <= fills; ++x) {
@@ -623,6 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (M::kind == 0 && asked == read) ask();
                 }
                 if (M::kind != 0 && x == ask_at && asked == read) ask();
+                // Causal attention has its fills written in another way: with those of the
+                // other masks below an 8K prompt takes 348 us (341), two chunks over 16K 181
+                // (178), five drafted tokens 120.4 (119.3); asking late then 346, 181, 120.2.
                 if constexpr (M::kind == 0) {
                     const int st = fill % C::STAGES;
                     const uint32_t use = fill / C::STAGES;

@@ -124,7 +124,8 @@ typedef struct {
  * 152 SMs at d = 128, less for caches of short units), so that no call
  * allocates.  Synchronous.
  * On success *out owns all of it.
- * Errors: INVALID_ARG (config), UNSUPPORTED (G or d or dtype), OUT_OF_MEMORY. */
+ * Errors: INVALID_ARG (config), UNSUPPORTED (G or d or dtype, more than 65535 units, a
+ * pool of 2^31 K and V rows), OUT_OF_MEMORY. */
 hikv_status hikv_create_cache(const hikv_config* cfg, hikv_cache** out);
 
 /* Free everything the cache owns (synchronises the device first).  NULL is a no-op. */
@@ -419,9 +420,10 @@ hikv_status hikv_tree_masks(hikv_cache* cache, const int32_t* ntok_host, const i
 /* hikv_append_packed of tree nodes: k and q are rotated by the position of the
  * sequence's first node plus depth[row] (DEVICE [sum ntok], 0 <= depth < the
  * sequence's ntok; others are clamped and reported as HIKV_ERR_STATE by
- * hikv_device_status).  The nodes take the unit's next slots and, as far as the
- * other calls are concerned, its next positions, in the order given, until
- * hikv_accept or hikv_drop.
+ * hikv_device_status).  The tables must reach ntok positions from the first node's
+ * on, whatever the depths are (they are on the device).  The nodes take the unit's
+ * next slots and, as far as the other calls are concerned, its next positions, in
+ * the order given, until hikv_accept or hikv_drop.
  * Errors: as hikv_append_packed, INVALID_ARG (null depth or rope). */
 hikv_status hikv_append_tree(hikv_cache* cache, int32_t layer, const int32_t* ntok_host, const int32_t* depth,
                              const hikv_rows* k, const hikv_rows* v, const hikv_rows* q, const hikv_rows* q_out,
@@ -433,7 +435,8 @@ hikv_status hikv_append_tree(hikv_cache* cache, int32_t layer, const int32_t* nt
  * the sequence's nq.  For the nodes of hikv_append_tree with the masks of
  * hikv_tree_masks, or masks of the caller's own, in any shape; bits from nq_host[b]
  * on are ignored; mask must not overlap out.  A token that sees nothing (no bit set,
- * nothing in front) gets a row of zeros.  Everything else as by hikv_attend_packed.
+ * nothing in front) gets a row of zeros (one whose logits are all -inf NaN, as by the
+ * other calls).  Everything else as by hikv_attend_packed.
  * Errors: as hikv_attend_packed, INVALID_ARG (null or misaligned mask, nq above 32 words). */
 hikv_status hikv_attend_tree(hikv_cache* cache, int32_t layer, const int32_t* nq_host, const uint32_t* mask,
                              int32_t words, const hikv_rows* q, const hikv_rows* out, hikv_stream_t stream);
