@@ -57,7 +57,7 @@
 // masked by a word of bits for each 32 keys of a row, worked out by the row's
 // own thread; the keys between the first tokens and an item's window are left
 // out of its key numbers, so that they cost neither a load nor a product.
-// Measured: 64 tree nodes over eight 8K-32K caches 140 to 162 us, by box (4.5 to 5.2
+// Measured: 64 tree nodes over eight 8K-32K caches 140 to 162 us, by GPU (4.5 to 5.2
 // TB/s); a 16K prompt in windows of 1024, 32/8 heads, 206 to 226 us (1.18 to 1.30
 // PFLOP/s of what is seen); one token of 64 sequences in windows of 2044 98 us (5.5
 // TB/s).  A mask costs 600 to 1,000
